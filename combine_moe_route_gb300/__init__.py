@@ -16,6 +16,8 @@ _API = {
     "moe_layer", "library_path", "load_library", "MOE_OK", "dispatch_noalloc",
     "route_topk_grouped", "dispatch_ll", "combine_ll", "combine_ll_push", "DispatchLLResult",
     "combine_partial_send", "combine_partial_recv", "BoundLayer",
+    "expert_gemm", "expert_gated_gemm", "expert_gated_backward", "combine_backward", "dispatch_backward",
+    "GatedResult", "CombineGrad",
 }
 
 __all__ = sorted(_API) + ["workloads", "HostLayerPipeline"]

@@ -99,6 +99,16 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.moe_get_device_error.restype = i32
         lib.moe_dispatch_noalloc.argtypes = [vp, vp, i32, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.moe_dispatch_noalloc.restype = i32
+        lib.moe_expert_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+        lib.moe_expert_gemm.restype = i32
+        lib.moe_expert_gated_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+        lib.moe_expert_gated_gemm.restype = i32
+        lib.moe_expert_gated_backward.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp]
+        lib.moe_expert_gated_backward.restype = i32
+        lib.moe_combine_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, i32, vp, vp, vp, vp, vp]
+        lib.moe_combine_backward.restype = i32
+        lib.moe_dispatch_backward.argtypes = [vp, vp, i32, i32, i32, i64, i32, vp, vp]
+        lib.moe_dispatch_backward.restype = i32
         for reader in ("moe_trace_dispatch", "moe_trace_combine"):   # builds with -DMOE_TRACE only
             try:
                 fn = getattr(lib, reader)
@@ -696,4 +706,219 @@ def dispatch_noalloc(x: torch.Tensor, topk_idx: torch.Tensor, B, E: int, *, fp8:
                   _ptr(out.recv_x), _ptr(out.recv_scale) if fp8 else None, _ptr(out.counts), _ptr(out.offsets),
                   _ptr(out.expert_offsets), _ptr(out.tok2row), _ptr(out.row2src),
                   _stream_handle(stream, x.device)), "moe_dispatch_noalloc")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# expert products (e4m3, fp32 scales per 128 channels and per 128 x 128 block)
+# ---------------------------------------------------------------------------
+
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _nblocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def _on(t: torch.Tensor, *others: torch.Tensor | None) -> None:
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
+
+
+def _expert_operands(a, a_scale, w, w_scale, expert_offsets, transpose):
+    _dev(a, "a", _E4M3)
+    _dev(w, "w", _E4M3)
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, C] and w [E, N, C] ([E, C, N] with transpose)")
+    rows, C = a.shape
+    E = w.shape[0]
+    N, c = (w.shape[2], w.shape[1]) if transpose else (w.shape[1], w.shape[2])
+    if c != C:
+        raise ValueError(f"a has {C} channels, the weight contracts over {c}")
+    _dev(a_scale, "a_scale", torch.float32, (rows, _nblocks(C)))
+    _dev(w_scale, "w_scale", torch.float32, (E, _nblocks(w.shape[1]), _nblocks(w.shape[2])))
+    _dev(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    _on(a, a_scale, w, w_scale, expert_offsets)
+    return rows, E, N, C
+
+
+def expert_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                expert_offsets: torch.Tensor, *, transpose: bool = False, out_dtype: torch.dtype = torch.bfloat16,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The experts' product over rows grouped by expert -> [rows, N].
+
+    ``a`` [rows, C] e4m3 with ``a_scale`` [rows, C/128], ``w`` [E, N, C] e4m3 with ``w_scale``
+    [E, N/128, C/128]; rows [expert_offsets[e], expert_offsets[e+1]) meet ``w[e]``.  With
+    ``transpose`` the weight is [E, C, N] and the product contracts over its rows: the gradient
+    of the forward's input, from the forward's own weight."""
+    rows, E, N, C = _expert_operands(a, a_scale, w, w_scale, expert_offsets, transpose)
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
+    _dev(out, "out", out_dtype, (rows, N))
+    _on(a, out)
+    with torch.cuda.device(a.device):
+        _check(load_library().moe_expert_gemm(
+            _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(expert_offsets), E, N, C, rows, int(bool(transpose)),
+            _DTYPE_FP32 if out_dtype == torch.float32 else _DTYPE_BF16, _ptr(out), _stream_handle(stream, a.device)),
+            "moe_expert_gemm")
+    return out
+
+
+@dataclass
+class GatedResult:
+    q: torch.Tensor             # [rows, I] e4m3: silu(gate) * up, quantised
+    scale: torch.Tensor         # [rows, I/128] fp32
+    h: torch.Tensor | None      # [rows, 2I] bf16: gate and up before the gate, where kept
+
+
+def expert_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                      expert_offsets: torch.Tensor, *, save_h: bool = False, out: torch.Tensor | None = None,
+                      out_scale: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                      stream=None) -> GatedResult:
+    """The gated first product: quantise(silu(a wg^T) * (a wu^T)) for ``w`` = [E, 2I, C], the
+    gate's I rows first.  ``save_h`` (or a buffer ``h``) keeps the products in bf16 for
+    ``expert_gated_backward``."""
+    rows, E, N, C = _expert_operands(a, a_scale, w, w_scale, expert_offsets, False)
+    if N % 256:
+        raise ValueError("w must be [E, 2*I, C] with I a multiple of 128")
+    inner, dev = N // 2, a.device
+    if out is None:
+        out = torch.empty((rows, inner), dtype=torch.float8_e4m3fn, device=dev)
+    if out_scale is None:
+        out_scale = torch.empty((rows, inner // 128), dtype=torch.float32, device=dev)
+    if h is None and save_h:
+        h = torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
+    _dev(out, "out", _E4M3, (rows, inner))
+    _dev(out_scale, "out_scale", torch.float32, (rows, inner // 128))
+    if h is not None:
+        _dev(h, "h", torch.bfloat16, (rows, N))
+    _on(a, out, out_scale, h)
+    with torch.cuda.device(dev):
+        _check(load_library().moe_expert_gated_gemm(
+            _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(expert_offsets), E, inner, C, rows, _ptr(out),
+            _ptr(out_scale), _ptr(h), _stream_handle(stream, dev)), "moe_expert_gated_gemm")
+    return GatedResult(out, out_scale, h)
+
+
+# ---------------------------------------------------------------------------
+# gradients
+# ---------------------------------------------------------------------------
+
+def expert_gated_backward(h: torch.Tensor, dv: torch.Tensor, *, fp8: bool = True, out: torch.Tensor | None = None,
+                          out_scale: torch.Tensor | None = None, stream=None):
+    """Gradient of v = silu(gate) * up: (dh [rows, 2I], its scales or None), dh quantised for the
+    transposed ``expert_gemm`` (``fp8``) or bf16."""
+    _dev(h, "h", torch.bfloat16)
+    if h.dim() != 2 or h.shape[1] % 2:
+        raise ValueError("h must be [rows, 2*I]")
+    rows, inner = h.shape[0], h.shape[1] // 2
+    _dev(dv, "dv", torch.bfloat16, (rows, inner))
+    dev = h.device
+    if out is None:
+        out = torch.empty((rows, 2 * inner), dtype=torch.float8_e4m3fn if fp8 else torch.bfloat16, device=dev)
+    _dev(out, "out", _E4M3 if fp8 else torch.bfloat16, (rows, 2 * inner))
+    if fp8:
+        if out_scale is None:
+            out_scale = torch.empty((rows, 2 * inner // 128), dtype=torch.float32, device=dev)
+        _dev(out_scale, "out_scale", torch.float32, (rows, 2 * inner // 128))
+    else:
+        out_scale = None
+    _on(h, dv, out, out_scale)
+    with torch.cuda.device(dev):
+        _check(load_library().moe_expert_gated_backward(
+            _ptr(h), _ptr(dv), rows, inner, _DTYPE_FP8 if fp8 else _DTYPE_BF16, _ptr(out), _ptr(out_scale),
+            _stream_handle(stream, dev)), "moe_expert_gated_backward")
+    return out, out_scale
+
+
+@dataclass
+class CombineGrad:
+    dy: torch.Tensor                # [rows, H] bf16 or e4m3
+    dy_scale: torch.Tensor | None   # [rows, H/128] fp32 (FP8 only)
+    dtopk_w: torch.Tensor           # [T, K] fp32
+    dlogits: torch.Tensor | None    # [T, E] fp32, where asked for
+
+
+def combine_backward(dout: torch.Tensor, y: torch.Tensor, tok2row: torch.Tensor | None, topk_w: torch.Tensor, *,
+                     topk_idx: torch.Tensor | None = None, E: int | None = None, fp8: bool = False,
+                     out: torch.Tensor | None = None, out_scale: torch.Tensor | None = None,
+                     dtopk_w: torch.Tensor | None = None, dlogits: torch.Tensor | None = None,
+                     stream=None) -> CombineGrad:
+    """Gradient of ``combine`` / ``combine_ll``: dy[tok2row[g*K+j]] = topk_w[g,j] * dout[g] (bf16,
+    or quantised with ``fp8``), dtopk_w[g,j] = <dout[g], y[row]> and, with ``topk_idx`` and
+    ``E``, the gradient of the router's logits through their softmax.  Rows of dy that no copy
+    maps to (the low-latency layout's free slots) are left as they are."""
+    _dev(dout, "dout", torch.bfloat16)
+    _dev(y, "y", torch.bfloat16)
+    _dev(topk_w, "topk_w", torch.float32)
+    if dout.dim() != 2 or y.dim() != 2 or topk_w.dim() != 2:
+        raise ValueError("dout must be [T, H], y [rows, H] and topk_w [T, K]")
+    T, K = topk_w.shape
+    rows, H = y.shape
+    if dout.shape != (T, H):
+        raise ValueError(f"dout must have shape {(T, H)}, got {tuple(dout.shape)}")
+    if tok2row is not None:
+        _dev(tok2row, "tok2row", torch.int32)
+        if tok2row.numel() != T * K:
+            raise ValueError("tok2row must have T*K entries")
+    dev = y.device
+    if out is None:
+        out = torch.empty((rows, H), dtype=torch.float8_e4m3fn if fp8 else torch.bfloat16, device=dev)
+    _dev(out, "out", _E4M3 if fp8 else torch.bfloat16, (rows, H))
+    if fp8:
+        if out_scale is None:
+            out_scale = torch.empty((rows, H // 128), dtype=torch.float32, device=dev)
+        _dev(out_scale, "out_scale", torch.float32, (rows, H // 128))
+    else:
+        out_scale = None
+    if dtopk_w is None:
+        dtopk_w = torch.empty((T, K), dtype=torch.float32, device=dev)
+    _dev(dtopk_w, "dtopk_w", torch.float32, (T, K))
+    if (topk_idx is None) != (E is None):
+        raise ValueError("the gradient of the logits needs both topk_idx and E")
+    if topk_idx is not None:
+        _dev(topk_idx, "topk_idx", torch.int32, (T, K))
+        if dlogits is None:
+            dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        _dev(dlogits, "dlogits", torch.float32, (T, E))
+    elif dlogits is not None:
+        raise ValueError("the gradient of the logits needs both topk_idx and E")
+    _on(y, dout, tok2row, topk_w, topk_idx, out, out_scale, dtopk_w, dlogits)
+    with torch.cuda.device(dev):
+        _check(load_library().moe_combine_backward(
+            _ptr(dout), _ptr(y), _ptr(tok2row), _ptr(topk_w), _ptr(topk_idx), T, K, H, rows, E or 0,
+            _DTYPE_FP8 if fp8 else _DTYPE_BF16, _ptr(out), _ptr(out_scale), _ptr(dtopk_w), _ptr(dlogits),
+            _stream_handle(stream, dev)), "moe_combine_backward")
+    return CombineGrad(out, out_scale, dtopk_w, dlogits)
+
+
+def dispatch_backward(drows: torch.Tensor, tok2row: torch.Tensor, K: int, *,
+                      out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Gradient of the dispatch scatter: dx[g] = sum_j drows[tok2row[g*K+j]] (fp32, j ascending)
+    -> [T, H] for T = tok2row.numel() / K."""
+    _dev(drows, "drows", torch.bfloat16)
+    if drows.dim() != 2:
+        raise ValueError("drows must be [rows, H]")
+    _dev(tok2row, "tok2row", torch.int32)
+    if K < 1 or tok2row.numel() % K:
+        raise ValueError("tok2row must have T*K entries")
+    T, (rows, H) = tok2row.numel() // K, drows.shape
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=drows.device)
+    _dev(out, "out", out_dtype, (T, H))
+    _on(drows, tok2row, out)
+    with torch.cuda.device(drows.device):
+        _check(load_library().moe_dispatch_backward(
+            _ptr(drows), _ptr(tok2row), T, K, H, rows, _DTYPE_FP32 if out_dtype == torch.float32 else _DTYPE_BF16,
+            _ptr(out), _stream_handle(stream, drows.device)), "moe_dispatch_backward")
     return out

@@ -55,7 +55,8 @@ __device__ __forceinline__ void fma_row(float (&acc)[8], float w, const uint4 v)
 }
 
 // tok2row == nullptr reads row g*K + j (the layout a push-style return leaves
-// on the origin rank); rows = number of rows of y (indices outside are skipped).
+// on the origin rank); topk_w == nullptr weighs every row by 1, the gradient of
+// the dispatch scatter (moe_dispatch_backward); rows = number of rows of y (indices outside are skipped).
 // kAfterWait: launched with programmatic stream serialization behind the
 // combine receive half's wait kernel; nothing is read before that grid is done.
 template <bool kOutF32, bool kAfterWait = false>
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __nv_bfl
         if (threadIdx.x < K) {
             const long long r = tok2row ? (long long)__ldg(tok2row + g * K + threadIdx.x) : g * K + threadIdx.x;
             s_row[threadIdx.x] = (r >= 0 && r < rows) ? (int32_t)r : -1;
-            s_w[threadIdx.x] = __ldg(topk_w + g * K + threadIdx.x);
+            s_w[threadIdx.x] = topk_w ? __ldg(topk_w + g * K + threadIdx.x) : 1.0f;
         }
         __syncthreads();
 

@@ -66,6 +66,7 @@ extern "C" {
 #define MOE_MAX_TOPK 32        /* K */
 #define MOE_MAX_HIDDEN 16384   /* H */
 #define MOE_MAX_GROUPS 32      /* expert groups of moe_route_topk_grouped */
+#define MOE_MAX_EXPERT_DIM 65536 /* either dimension of an expert's weight */
 
 /* A CUDA stream (the same type as cudaStream_t); NULL is the legacy default stream. */
 typedef struct CUstream_st *moe_stream_t;
@@ -474,6 +475,134 @@ MOE_API moe_status moe_combine_send(int R, void *workspace, size_t workspace_byt
 MOE_API moe_status moe_combine_recv(const void *y, const int32_t *tok2row, const float *topk_w, int T, int K, int H,
                                     moe_dtype out_dtype, void *out, int R, void *workspace, size_t workspace_bytes,
                                     moe_stream_t stream);
+
+/*
+ * moe_expert_gemm -- the experts' product over rows grouped by expert, in
+ * e4m3 with one fp32 scale per 128 channels of a row and per 128 x 128 block
+ * of a weight ([DSD] "Quantization": block-wise FP8; "GroupGEMM": one product
+ * per local expert over the rows dispatch packed for it).  The rows and scales
+ * are those of an FP8 moe_dispatch, of moe_expert_gated_gemm or of the
+ * quantising gradients below.
+ *
+ *   a          device e4m3 [rows, C], 16-byte aligned.
+ *   a_scale    device fp32 [rows, ceil(C/128)].
+ *   w          device e4m3, 16-byte aligned: [E, N, C], or [E, C, N] with
+ *              transpose != 0.
+ *   w_scale    device fp32 [E, ceil(N/128), ceil(C/128)], or
+ *              [E, ceil(C/128), ceil(N/128)] with transpose != 0.
+ *   expert_offsets device int32 [E + 1], non-decreasing, from moe_dispatch:
+ *              expert e owns rows [expert_offsets[e], expert_offsets[e+1]).
+ *              An expert without rows is legal and its weight is not read.
+ *              Entries outside [0, rows] are clamped to it.
+ *   E          experts, 1..MOE_MAX_EXPERTS.
+ *   N, C       columns of the result and length of the contraction, multiples
+ *              of 16 in 16..MOE_MAX_EXPERT_DIM.
+ *   rows       rows of a and out, >= 0 (0 enqueues nothing).
+ *   transpose  0: out = a x w[e]^T, the forward product.  Otherwise out =
+ *              a x w[e]: with the forward's weight and the quantised gradient
+ *              of its result as a, the gradient of its input.
+ *   out_dtype  MOE_DTYPE_BF16 or MOE_DTYPE_FP32.
+ *   out        device [rows, N] of out_dtype, 16-byte aligned: for row r of
+ *              expert e, with b over the 128-channel blocks of C,
+ *                out[r, n] = sum_b a_scale[r, b] * w_scale[e, n/128, b]
+ *                            * sum_{c in b} a[r, c] * w[e, n, c]
+ *              (w_scale[e, b, n/128] and w[e, c, n] with transpose), all sums
+ *              in fp32, rounded once.  Rows no expert owns are not written.
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_expert_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
+                                   const int32_t *expert_offsets, int E, int N, int C, int rows, int transpose,
+                                   moe_dtype out_dtype, void *out, moe_stream_t stream);
+
+/*
+ * moe_expert_gated_gemm -- the first product of a gated expert, its gate and
+ * the quantisation of the result for the second product, in one pass.  The
+ * weight holds the gate's I rows, then the up projection's I rows; with
+ * p = the fp32 result of moe_expert_gemm's formula for N = 2*I,
+ *     v[r, i] = silu(p[r, i]) * p[r, I + i],  silu(z) = z / (1 + exp(-z)),
+ * and q, q_scale are v quantised per 128 channels of a row by moe_dispatch's
+ * rule (a NaN in a block becomes a NaN code and does not enter its amax).
+ *
+ *   a, a_scale, w, w_scale, expert_offsets, E, C, rows   as moe_expert_gemm
+ *              (w [E, 2*I, C], w_scale [E, 2*I/128, ceil(C/128)]).
+ *   I          a multiple of 128 in 128..MOE_MAX_EXPERT_DIM/2.
+ *   q          device e4m3 [rows, I], 16-byte aligned: out.
+ *   q_scale    device fp32 [rows, I/128]: out.
+ *   h          device bf16 [rows, 2*I], 16-byte aligned, or NULL: out, p
+ *              rounded to bf16 for moe_expert_gated_backward.
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_expert_gated_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
+                                         const int32_t *expert_offsets, int E, int I, int C, int rows, void *q,
+                                         float *q_scale, void *h, moe_stream_t stream);
+
+/*
+ * moe_expert_gated_backward -- gradient of the gate.  With (g, u) the halves of
+ * a row of h, s = 1 / (1 + exp(-g)) and dv the gradient of v = silu(g) * u,
+ *     dg = dv * u * s * (1 + g * (1 - s)),   du = dv * g * s   (fp32),
+ * and dh = [dg, du], in bf16 or quantised per 128 channels by moe_dispatch's
+ * rule: the operand of the transposed moe_expert_gemm.
+ *
+ *   h          device bf16 [rows, 2*I], 16-byte aligned.
+ *   dv         device bf16 [rows, I], 16-byte aligned.
+ *   I          a multiple of 8 (of 128 for FP8) in 8..MOE_MAX_EXPERT_DIM/2.
+ *   dh_dtype   MOE_DTYPE_BF16 or MOE_DTYPE_FP8_E4M3.
+ *   dh         device [rows, 2*I] of dh_dtype, 16-byte aligned: out.
+ *   dh_scale   device fp32 [rows, 2*I/128]: out, FP8 only (may be NULL for bf16).
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_expert_gated_backward(const void *h, const void *dv, int rows, int I, moe_dtype dh_dtype,
+                                             void *dh, float *dh_scale, moe_stream_t stream);
+
+/*
+ * moe_combine_backward -- gradient of moe_combine (and, with rows = E*R*C, of
+ * moe_combine_ll): to the expert outputs, the routing weights and, where
+ * wanted, the router's logits.
+ *
+ *   dout       device bf16 [T, H], 16-byte aligned: gradient of the output.
+ *   y          device bf16 [rows, H], 16-byte aligned: combine's expert outputs.
+ *   tok2row, topk_w   as moe_combine (tok2row NULL: the identity map); the
+ *              entries of tok2row inside [0, rows) are distinct.
+ *   topk_idx   device int32 [T, K], only read for dlogits (else may be NULL).
+ *   rows       rows of y and dy, >= 0 and < 2^31.
+ *   E          experts, 1..MOE_MAX_EXPERTS (only checked for dlogits).
+ *   dy_dtype   MOE_DTYPE_BF16, or MOE_DTYPE_FP8_E4M3 (H % 128 == 0) quantised
+ *              per 128 channels by moe_dispatch's rule.
+ *   dy         device [rows, H] of dy_dtype, 16-byte aligned: out,
+ *              dy[tok2row[g*K+j]] = topk_w[g,j] * dout[g] (fp32 product,
+ *              rounded once).  Rows no copy maps to are not written.
+ *   dy_scale   device fp32 [rows, H/128]: out, FP8 only.
+ *   dtopk_w    device fp32 [T, K]: out, sum_h dout[g,h] * y[tok2row[g*K+j], h]
+ *              in fp32, in an order that does not change from call to call; 0
+ *              where tok2row is outside [0, rows).
+ *   dlogits    device fp32 [T, E] or NULL: out, the gradient through
+ *              moe_route_topk[_grouped]'s softmax over the selected logits:
+ *              w_j * (dw_j - sum_i w_i dw_i) at expert topk_idx[g,j], 0
+ *              elsewhere.
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.  T == 0
+ * enqueues nothing.
+ */
+MOE_API moe_status moe_combine_backward(const void *dout, const void *y, const int32_t *tok2row, const float *topk_w,
+                                        const int32_t *topk_idx, int T, int K, int H, int64_t rows, int E,
+                                        moe_dtype dy_dtype, void *dy, float *dy_scale, float *dtopk_w, float *dlogits,
+                                        moe_stream_t stream);
+
+/*
+ * moe_dispatch_backward -- gradient of the dispatch scatter (of any layout):
+ *     dx[g] = sum_{j=0..K-1} drows[tok2row[g*K+j]],
+ * accumulated in fp32 in the order j = 0..K-1 from +0, then rounded to bf16 or
+ * stored as fp32.  (The FP8 dispatch's quantisation passes its gradient
+ * through unchanged.)
+ *
+ *   drows      device bf16 [rows, H], 16-byte aligned: gradient of recv_x.
+ *   tok2row    device int32 [T*K]; entries outside [0, rows) contribute nothing.
+ *   rows       >= 0 and < 2^31.
+ *   out_dtype  MOE_DTYPE_BF16 or MOE_DTYPE_FP32.
+ *   dx         device [T, H] of out_dtype, 16-byte aligned: out.
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_dispatch_backward(const void *drows, const int32_t *tok2row, int T, int K, int H, int64_t rows,
+                                         moe_dtype out_dtype, void *dx, moe_stream_t stream);
 
 /*
  * moe_get_device_error -- SYNCHRONOUS: waits for `stream`, then copies the

@@ -17,7 +17,7 @@ _API = {
     "route_topk_grouped", "dispatch_ll", "combine_ll", "combine_ll_push", "DispatchLLResult",
     "combine_partial_send", "combine_partial_recv", "BoundLayer",
     "expert_gemm", "expert_gated_gemm", "expert_gated_backward", "combine_backward", "dispatch_backward",
-    "GatedResult", "CombineGrad",
+    "GatedResult", "CombineGrad", "get_expert_error",
 }
 
 __all__ = sorted(_API) + ["workloads", "HostLayerPipeline"]

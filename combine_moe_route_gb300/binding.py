@@ -103,6 +103,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.moe_expert_gemm.restype = i32
         lib.moe_expert_gated_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
         lib.moe_expert_gated_gemm.restype = i32
+        lib.moe_get_expert_error.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
+        lib.moe_get_expert_error.restype = i32
         lib.moe_expert_gated_backward.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp]
         lib.moe_expert_gated_backward.restype = i32
         lib.moe_combine_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, i32, vp, vp, vp, vp, vp]
@@ -803,6 +805,16 @@ def expert_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w
             _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(expert_offsets), E, inner, C, rows, _ptr(out),
             _ptr(out_scale), _ptr(h), _stream_handle(stream, dev)), "moe_expert_gated_gemm")
     return GatedResult(out, out_scale, h)
+
+
+def get_expert_error(device=None, stream=None) -> tuple[int, int]:
+    """Synchronise the stream, read and clear the device's error word of the expert products:
+    (status, raw bits)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    code = ctypes.c_int32(0)
+    with torch.cuda.device(dev):
+        st = load_library().moe_get_expert_error(ctypes.byref(code), _stream_handle(stream, dev))
+    return int(st), int(code.value)
 
 
 # ---------------------------------------------------------------------------

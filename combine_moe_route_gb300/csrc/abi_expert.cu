@@ -47,6 +47,12 @@ moe_status moe_expert_gated_gemm(const void *a, const float *a_scale, const void
                                                      h, (cudaStream_t)stream));
 }
 
+moe_status moe_get_expert_error(int32_t *host_code, moe_stream_t stream) {
+    if (!host_code) return MOE_ERR_INVALID_ARG;
+    if (moe::read_product_error(host_code, (cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
+    return *host_code ? MOE_ERR_TIMEOUT : MOE_OK;
+}
+
 moe_status moe_expert_gated_backward(const void *h, const void *dv, int rows, int I, moe_dtype dh_dtype, void *dh,
                                      float *dh_scale, moe_stream_t stream) {
     if (rows < 0 || I < 8 || I > MOE_MAX_EXPERT_DIM / 2 || I % 8 != 0) return MOE_ERR_INVALID_ARG;

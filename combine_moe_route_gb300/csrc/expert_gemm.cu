@@ -2,171 +2,572 @@
 // grouped by expert, in e4m3 with fp32 scales per 128 channels of a row and
 // per 128 x 128 block of a weight.
 //
-// Plain tiled form: a block computes 64 rows x 128 columns (for the gated form
-// 128 columns of each half) of one expert from tiles of e4m3 values held as
-// fp32 in shared memory.  The values of a 128-channel block are summed as they
-// are and the block's sum is scaled once, a_scale * w_scale, into the result.
+//   p[r, n] = sum_b a_scale[r, b] * w_scale[e, n/128, b] * sum_{c in b} a[r, c] * w[e, n, c]
+//
+// The scales are general fp32 values, so they cannot ride in the tensor
+// cores' own block scaling (powers of two): the inner sum over a block of 128
+// channels runs on the tensor cores into a fresh fp32 accumulator, and the
+// outer sum adds that accumulator, times the two scales, to registers.
+//
+// A persistent block per SM walks output tiles of 128 rows of one expert x kBN
+// columns.  Its warps have fixed jobs:
+//   warp 0      loads the e4m3 tiles of both operands, 128 channels a stage,
+//               with tiled bulk tensor copies into a ring of stages;
+//   warp 1      issues the products of a stage (4 x K = 32) into one of the
+//               tensor memory's accumulators, which alternate stage by stage;
+//   warps 4-11  (two warpgroups) read a finished accumulator, one row per
+//               thread and kBN / 2 columns per warpgroup, scale it into
+//               registers, and after the last stage write the tile.
+// A row tile that is not full loads only the groups of 32 rows it has; rows of
+// an accumulator past them hold leftovers that nothing reads (a row of the
+// result depends on its own row of A alone).
+//
+// The forward weight [E, N, C] is a K-major operand.  The transposed product
+// reads the same weight, [E, C, N] in its terms, as an MN-major operand, so
+// no transposed copy is made.
+//
+// The gated form takes 128 columns of the gate and the 128 of the up
+// projection as one tile of 256: each warpgroup holds 64 of both, forms
+// silu(g) * u in fp32, and the two exchange their maxima of a row to quantise
+// its block of 128.
+#include <atomic>
+
 #include "launch.h"
 #include "numeric.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
-constexpr int kTileM = 64, kTileN = 128, kTileK = 32;
+constexpr int kProductThreads = 384;
+constexpr int kRowTile = 128;     // rows of a tile: the M of one product
+constexpr int kRowGroup = 32;     // rows per load of A
+constexpr int kBlockK = 128;      // channels per stage: one scale block, 128 bytes
+constexpr int kStageA = kRowTile * kBlockK;
+constexpr int kWeightBox = 128 * kBlockK;   // bytes of one load of the weight: 128 columns x 128 channels
+constexpr int kTmemColumns = 512;
+constexpr int kStagingWarp = 16 * 128;      // output staging of a warp: 16 rows x 128 bytes
+
+// Set when a bounded wait of a product kernel ran out (never in a sound run).
+__device__ int32_t g_product_error;
 
 struct ProductArgs {
-    const unsigned char *a, *w;
     const float *a_scale, *w_scale;
     const int32_t *expert_offsets;
-    int E, N, C;        // out[rows, N] = a[rows, C] x weight
-    long long rows;
-    bool transpose;     // weight is [E, C, N] (contraction over its rows) instead of [E, N, C]
+    int E, N, C;
+    int rows;
+    int ntiles;         // column tiles
     bool out_f32;
-    void *out;          // plain form
+    void *out;          // plain form: [rows, N]
     unsigned char *q;   // gated form: [rows, N / 2]
     float *q_scale;
-    __nv_bfloat16 *h;
+    __nv_bfloat16 *h;   // gated form: [rows, N] or null
 };
 
-__device__ __forceinline__ float weight_at(const ProductArgs &p, int e, int n, int c) {
-    if (n >= p.N || c >= p.C) return 0.0f;
-    return e4m3_to_float(p.w[p.transpose ? ((size_t)e * p.C + c) * p.N + n : ((size_t)e * p.N + n) * p.C + c]);
-}
+template <int kBN>
+struct ProductLayout {
+    static constexpr int kStageBytes = kStageA + kBN * kBlockK;
+    static constexpr int kStages = 192 * 1024 / kStageBytes;
+    static constexpr int kBuffers = kTmemColumns / kBN;
+    static constexpr int kStaging = kStages * kStageBytes;
+    static constexpr int kBytes = kStaging + 8 * kStagingWarp + 1024;   // + alignment of the swizzled tiles
+};
 
-// The scale of the weight block that holds output column n and channel block b.
-__device__ __forceinline__ float weight_scale_at(const ProductArgs &p, int e, int n, int b) {
-    const int nb = (p.N + 127) / 128, cb = (p.C + 127) / 128;
-    return __ldg(p.w_scale + (p.transpose ? ((size_t)e * cb + b) * nb + n / 128 : ((size_t)e * nb + n / 128) * cb + b));
-}
+template <int kBN>
+struct ProductShared {
+    uint64_t full[ProductLayout<kBN>::kStages], empty[ProductLayout<kBN>::kStages];
+    uint64_t acc_full[ProductLayout<kBN>::kBuffers], acc_empty[ProductLayout<kBN>::kBuffers];
+    uint64_t pair[4];                      // gated: the two warps that share a quarter of the rows
+    uint64_t drain;
+    uint32_t tmem;
+    volatile int32_t stop;                 // a wait ran out: every role leaves
+    int32_t warp_tiles[kProductThreads / 32];
+    int32_t tiles[MOE_MAX_EXPERTS + 1];    // row tiles before expert e
+    float amax[2][2][kRowTile];            // gated: by tile parity, each warpgroup's maximum of a row's block
+};
 
-template <bool kGated>
-__global__ void __launch_bounds__(256) expert_product_kernel(const ProductArgs p) {
-    constexpr int kSides = kGated ? 2 : 1;
-    __shared__ float s_a[kTileK][kTileM];
-    __shared__ float s_w[kSides][kTileK][kTileN];
-    __shared__ int s_e, s_row0, s_end;
-    if (threadIdx.x == 0) {   // which expert's m-tile blockIdx.y is
-        long long t = blockIdx.y;
-        s_e = -1;
-        for (int e = 0; e < p.E; ++e) {
-            const int lo = min(max(p.expert_offsets[e], 0), (int)p.rows), hi = min(max(p.expert_offsets[e + 1], 0), (int)p.rows);
-            const int tiles = hi > lo ? (hi - lo + kTileM - 1) / kTileM : 0;
-            if (t < tiles) {
-                s_e = e;
-                s_row0 = lo + (int)t * kTileM;
-                s_end = hi;
-                break;
-            }
-            t -= tiles;
+// Wait for a barrier's phase; false once any wait of the block has run out.
+template <class Shared>
+__device__ __forceinline__ bool wait_or_stop(Shared &s, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (s.stop) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            s.stop = 1;
+            atomicOr(&g_product_error, MOE_DEVERR_COPY_TIMEOUT);
+            return false;
         }
     }
-    __syncthreads();
-    if (s_e < 0) return;
-    const int e = s_e, row0 = s_row0, nvalid = min(s_end - row0, kTileM);
-    const int n0 = blockIdx.x * kTileN;
-    const int cb = (p.C + 127) / 128;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[kSides][4][8] = {}, sum[kSides][4][8] = {};
-    for (int c0 = 0; c0 < p.C; c0 += kTileK) {
-        for (int i = threadIdx.x; i < kTileM * kTileK; i += 256) {
-            const int r = i / kTileK, c = c0 + i % kTileK;
-            s_a[i % kTileK][r] = (r < nvalid && c < p.C) ? e4m3_to_float(p.a[(size_t)(row0 + r) * p.C + c]) : 0.0f;
+    return true;
+}
+
+// Position in a ring of n slots and the parity of its current pass.
+struct Ring {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void advance(int n) {
+        if (++slot == n) {
+            slot = 0;
+            parity ^= 1u;
         }
-        for (int s = 0; s < kSides; ++s)
-            for (int i = threadIdx.x; i < kTileN * kTileK; i += 256) {
-                const int n = p.transpose ? i % kTileN : i / kTileK, c = p.transpose ? i / kTileN : i % kTileK;
-                s_w[s][c][n] = weight_at(p, e, n0 + n + s * (p.N / 2), c0 + c);
+    }
+};
+
+struct Tile {
+    int e, row0, valid, n;   // expert, first row, rows, column tile
+};
+
+// Expert e's first row and number of rows, inside [0, rows] whatever the offsets hold.
+__device__ __forceinline__ int2 expert_rows(const ProductArgs &p, int e) {
+    const int lo = min(max(__ldg(p.expert_offsets + e), 0), p.rows);
+    const int hi = min(max(__ldg(p.expert_offsets + e + 1), 0), p.rows);
+    return make_int2(lo, max(hi - lo, 0));
+}
+
+// Tile t: experts in order; within an expert the row tiles of one column tile
+// come first, so that blocks working at the same time share the weight.
+template <class Shared>
+__device__ __forceinline__ Tile tile_at(const Shared &s, const ProductArgs &p, long long t) {
+    const int e = upper_bound_minus_one(s.tiles, p.E, (int)(t / p.ntiles));
+    const int mt = s.tiles[e + 1] - s.tiles[e];
+    const int i = (int)(t - (long long)s.tiles[e] * p.ntiles);
+    const int m = i % mt;
+    const int2 r = expert_rows(p, e);
+    return {e, r.x + m * kRowTile, min(r.y - m * kRowTile, kRowTile), i / mt};
+}
+
+// Writes the 16-byte chunks a lane holds of its row (32 rows of a warp, kChunks
+// each) to global memory in whole rows: 16 rows at a time through the warp's
+// staging, swizzled against bank conflicts, then kChunks lanes per row.  `dst`
+// is the address in the warp's row 0, rows lie `pitch` bytes apart; rows at or
+// past nrows and bytes at or past `limit` are not written.
+template <int kChunks>
+__device__ __forceinline__ void store_rows(const uint4 (&v)[kChunks], unsigned char *stage, unsigned char *dst,
+                                           size_t pitch, int nrows, int limit, int lane) {
+    constexpr int kRows = 32 / kChunks;   // rows per store instruction
+    const int c = lane % kChunks;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        __syncwarp();
+        if ((lane >> 4) == half) {
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k)
+                *reinterpret_cast<uint4 *>(stage + (lane & 15) * 128 + ((k ^ (lane & 7)) * 16)) = v[k];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16 / kRows; ++i) {
+            const int r = i * kRows + lane / kChunks;
+            const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((c ^ (r & 7)) * 16));
+            if (half * 16 + r < nrows && c * 16 < limit) st_v4(dst + (size_t)(half * 16 + r) * pitch + c * 16, x);
+        }
+    }
+}
+
+// 64 fp32 values of a row, as bf16.
+__device__ __forceinline__ void store_bf16x64(const float2 *acc, unsigned char *stage, unsigned char *dst, size_t pitch,
+                                              int nrows, int limit, int lane) {
+    uint4 v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        v[c] = make_uint4(bf16_pair(acc[4 * c].x, acc[4 * c].y), bf16_pair(acc[4 * c + 1].x, acc[4 * c + 1].y),
+                          bf16_pair(acc[4 * c + 2].x, acc[4 * c + 2].y), bf16_pair(acc[4 * c + 3].x, acc[4 * c + 3].y));
+    store_rows<8>(v, stage, dst, pitch, nrows, limit, lane);
+}
+
+template <int kBN, bool kTransposed, bool kGated>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    expert_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                          const ProductArgs p) {
+    using Layout = ProductLayout<kBN>;
+    extern __shared__ unsigned char s_raw[];
+    __shared__ ProductShared<kBN> s;
+    unsigned char *tiles = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);   // swizzled tiles: 1024-byte aligned
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nkb = (p.C + kBlockK - 1) / kBlockK;
+
+    // prologue: barriers, tensor memory, and the experts' row tiles
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Layout::kStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < Layout::kBuffers; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], 8);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&s.pair[i], 2);
+        mbar_init(&s.drain, 1);
+        s.stop = 0;
+        fence_mbarrier_init();
+        prefetch_tensor_map(&map_a);
+        prefetch_tensor_map(&map_w);
+    }
+    if (warp == 2) tmem_alloc<kTmemColumns>(&s.tmem);
+    {
+        constexpr int kPer = (MOE_MAX_EXPERTS + kProductThreads - 1) / kProductThreads;
+        int mine = 0, mt[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            mt[i] = 0;
+            if (e < p.E) mt[i] = (expert_rows(p, e).y + kRowTile - 1) / kRowTile;
+            mine += mt[i];
+        }
+        int sum = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += v;
+        }
+        if (lane == 31) s.warp_tiles[warp] = sum;
+        __syncthreads();
+        // 64 bits and a cap: offsets that overlap may not make the prefix wrap
+        long long before = sum - mine;
+        for (int w = 0; w < warp; ++w) before += s.warp_tiles[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            if (e < p.E) s.tiles[e] = (int)min(before, 1ll << 30);
+            before += mt[i];
+            if (e == p.E - 1) s.tiles[p.E] = (int)min(before, 1ll << 30);
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const long long total = (long long)s.tiles[p.E] * p.ntiles;
+    const uint32_t tmem = s.tmem;
+
+    if (warp < 4) {
+        registers_decrease<40>();
+        if (warp == 0 && lane == 0) {
+            // ---------------------------------------------------- loads
+            Ring r;
+            long long issued = 0;
+            bool go = true;
+            for (long long t = blockIdx.x; go && t < total; t += gridDim.x) {
+                const Tile tile = tile_at(s, p, t);
+                const int groups = (tile.valid + kRowGroup - 1) / kRowGroup;
+                const int n0 = tile.n * (kGated ? kBN / 2 : kBN);
+                const int boxes = kGated ? 2 : (min(kBN, p.N - n0) + 127) / 128;
+                const uint32_t bytes = groups * kRowGroup * kBlockK + boxes * kWeightBox;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!(go = wait_or_stop(s, &s.empty[r.slot], r.parity ^ 1u))) break;
+                    unsigned char *a = tiles + r.slot * Layout::kStageBytes, *w = a + kStageA;
+                    uint64_t *bar = &s.full[r.slot];
+                    mbar_arrive_expect_tx(bar, bytes);
+                    for (int i = 0; i < groups; ++i)
+                        tensor_load_2d(a + i * kRowGroup * kBlockK, &map_a, kb * kBlockK, tile.row0 + i * kRowGroup,
+                                       bar);
+                    for (int i = 0; i < boxes; ++i) {
+                        const int n = n0 + i * (kGated ? p.N / 2 : 128);
+                        if (kTransposed) tensor_load_3d(w + i * kWeightBox, &map_w, n, kb * kBlockK, tile.e, bar);
+                        else tensor_load_3d(w + i * kWeightBox, &map_w, kb * kBlockK, n, tile.e, bar);
+                    }
+                    r.advance(Layout::kStages);
+                    ++issued;
+                }
             }
-        __syncthreads();
-#pragma unroll 4
-        for (int c = 0; c < kTileK; ++c)
+            // nothing in flight when the block ends: the products have read every stage, or (after
+            // a wait ran out) at least its loads have landed
+            const int last = (int)(issued < Layout::kStages ? issued : Layout::kStages);
+            for (int i = 0; i < last; ++i) {
+                r.slot = (r.slot == 0 ? Layout::kStages : r.slot) - 1;
+                if (r.slot == Layout::kStages - 1) r.parity ^= 1u;
+                if (!wait_or_stop(s, &s.empty[r.slot], r.parity)) mbar_wait_bounded(&s.full[r.slot], r.parity);
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------- products
+            Ring r, b;
+            bool go = true;
+            for (long long t = blockIdx.x; go && t < total; t += gridDim.x) {
+                const Tile tile = tile_at(s, p, t);
+                const int cols = kGated ? kBN : min(kBN, p.N - tile.n * kBN);   // a multiple of 16
+                const uint32_t instruction = f8_instruction(kRowTile, cols, kTransposed);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!(go = wait_or_stop(s, &s.acc_empty[b.slot], b.parity ^ 1u))) break;
+                    if (!(go = wait_or_stop(s, &s.full[r.slot], r.parity))) break;
+                    tcgen05_fence_after();
+                    const uint32_t a = smem_u32(tiles) + r.slot * Layout::kStageBytes, w = a + kStageA;
 #pragma unroll
-            for (int s = 0; s < kSides; ++s)
+                    for (int k = 0; k < kBlockK / 32; ++k) {
+                        // 32 channels on: 32 bytes along a K-major row, 32 rows of 128 bytes MN-major
+                        const uint64_t da = smem_descriptor(a + k * 32, 16, 1024);
+                        const uint64_t dw = kTransposed ? smem_descriptor(w + k * 32 * 128, kWeightBox, 1024)
+                                                        : smem_descriptor(w + k * 32, 16, 1024);
+                        mma_f8(tmem + b.slot * kBN, da, dw, instruction, k > 0);
+                    }
+                    mma_commit(&s.empty[r.slot]);
+                    mma_commit(&s.acc_full[b.slot]);
+                    r.advance(Layout::kStages);
+                    b.advance(Layout::kBuffers);
+                }
+            }
+            if (!go) {   // leave no product running
+                mma_commit(&s.drain);
+                mbar_wait_bounded(&s.drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------- scaled sums and the output
+        registers_increase<232>();
+        constexpr int kCols = kBN / 2;            // columns of a warpgroup
+        const int wg = (warp >> 2) - 1, quarter = warp & 3;
+        unsigned char *stage = tiles + Layout::kStaging + (warp - 4) * kStagingWarp;
+        const int nb = (p.N + 127) / 128;         // scale blocks along the columns
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        Ring b;
+        uint32_t pair_parity = 0;
+        bool go = true;
+        for (long long t = blockIdx.x; go && t < total; t += gridDim.x) {
+            const Tile tile = tile_at(s, p, t);
+            const int nrows = min(tile.valid - quarter * 32, 32);   // rows of this warp
+            const int n0 = kGated ? tile.n * 128 : tile.n * kBN + wg * kCols;
+            const bool active = nrows > 0 && (kGated || n0 < p.N);
+            const size_t row = (size_t)tile.row0 + quarter * 32 + min(lane, max(nrows, 1) - 1);
+            const float *sa = p.a_scale + (active ? row : 0) * nkb;
+            // the weight scales of block b: sw[b * step] (and su for the up projection's block)
+            const size_t step = kTransposed ? nb : 1;
+            const int cblock = active ? n0 / 128 : 0;
+            const float *sw = p.w_scale + (kTransposed ? (size_t)tile.e * nkb * nb + cblock
+                                                       : ((size_t)tile.e * nb + cblock) * nkb);
+            const float *su = kGated ? sw + (size_t)(nb / 2) * nkb : nullptr;
+
+            float2 acc[kCols / 2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        sum[s][i][k] = __fmaf_rn(s_a[c][ty * 4 + i], s_w[s][c][tx + 16 * k], sum[s][i][k]);
-        __syncthreads();
-        if ((c0 + kTileK) % 128 != 0 && c0 + kTileK < p.C) continue;
-#pragma unroll
-        for (int s = 0; s < kSides; ++s) {   // the end of a block
-            const float sw = weight_scale_at(p, e, n0 + s * (p.N / 2), c0 / 128);
+            for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            // scales are fetched a group of four blocks ahead
+            float fa[4], fw[4], fu[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = min(ty * 4 + i, nvalid - 1);
-                const float f = __ldg(p.a_scale + (size_t)(row0 + r) * cb + c0 / 128) * sw;
+                fa[i] = i < nkb ? __ldg(sa + i) : 0.0f;
+                fw[i] = i < nkb ? __ldg(sw + i * step) : 0.0f;
+                if (kGated) fu[i] = i < nkb ? __ldg(su + i) : 0.0f;
+            }
+            for (int kb0 = 0; go && kb0 < nkb; kb0 += 4) {
+                float f[4], g[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    acc[s][i][k] = __fmaf_rn(f, sum[s][i][k], acc[s][i][k]);
-                    sum[s][i][k] = 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    f[i] = fa[i] * fw[i];
+                    if (kGated) g[i] = fa[i] * fu[i];
+                    const int kb = kb0 + 4 + i;
+                    if (kb < nkb) {
+                        fa[i] = __ldg(sa + kb);
+                        fw[i] = __ldg(sw + kb * step);
+                        if (kGated) fu[i] = __ldg(su + kb);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (kb0 + i >= nkb) break;
+                    go = __all_sync(0xffffffffu, wait_or_stop(s, &s.acc_full[b.slot], b.parity));
+                    if (!go) break;
+                    tcgen05_fence_after();
+                    if (active) {
+#pragma unroll
+                        for (int c = 0; c < kCols / 32; ++c) {
+                            const int col = kGated ? (c < 2 ? wg * 64 + c * 32 : 128 + wg * 64 + (c - 2) * 32)
+                                                   : wg * kCols + c * 32;
+                            const float fc = (kGated && c >= 2) ? g[i] : f[i];
+                            uint32_t v[32];
+                            tmem_load32(lanes + b.slot * kBN + col, v);
+                            tmem_wait_load();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                fma_pair(acc[c * 16 + k], make_float2(fc, fc),
+                                         make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+                        }
+                    }
+                    tcgen05_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.acc_empty[b.slot]);
+                    b.advance(Layout::kBuffers);
+                }
+            }
+            if (!go) break;
+            const size_t warp_row = (size_t)tile.row0 + quarter * 32;
+            if constexpr (kGated) {
+                const int I = p.N / 2, i0 = n0 + wg * 64;
+                if (p.h && active) {
+                    unsigned char *h = reinterpret_cast<unsigned char *>(p.h + warp_row * p.N + i0);
+                    store_bf16x64(acc, stage, h, (size_t)p.N * 2, nrows, 128, lane);
+                    store_bf16x64(acc + 32, stage, h + (size_t)I * 2, (size_t)p.N * 2, nrows, 128, lane);
+                }
+                float amax = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    acc[k].x = acc[k].x * sigmoid(acc[k].x) * acc[32 + k].x;
+                    acc[k].y = acc[k].y * sigmoid(acc[k].y) * acc[32 + k].y;
+                    amax = fmaxf(amax, fmaxf(fabsf(acc[k].x), fabsf(acc[k].y)));
+                }
+                // the two warps that hold a row swap their maxima; a warp writes a parity's slot
+                // again only after the other has arrived for the tile in between, so after its read
+                s.amax[pair_parity][wg][quarter * 32 + lane] = amax;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.pair[quarter]);
+                go = __all_sync(0xffffffffu, wait_or_stop(s, &s.pair[quarter], pair_parity));
+                if (!go) break;
+                amax = quant_amax(fmaxf(amax, s.amax[pair_parity][wg ^ 1][quarter * 32 + lane]));
+                pair_parity ^= 1u;
+                if (active) {
+                    const float inv = quant_inverse(amax);
+                    uint4 v[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 v0 = acc[c * 8 + 2 * k], v1 = acc[c * 8 + 2 * k + 1];
+                            w[k] = pack_e4m3x4(__fmul_rn(v0.x, inv), __fmul_rn(v0.y, inv), __fmul_rn(v1.x, inv),
+                                               __fmul_rn(v1.y, inv));
+                        }
+                        v[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    store_rows<4>(v, stage, p.q + warp_row * I + i0, I, nrows, 64, lane);
+                    if (wg == 0 && lane < nrows)
+                        p.q_scale[(warp_row + lane) * (I / 128) + tile.n] = quant_scale(amax);
+                }
+            } else if (active) {
+                if (p.out_f32) {
+#pragma unroll
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 v0 = acc[c * 16 + 2 * k], v1 = acc[c * 16 + 2 * k + 1];
+                            v[k] = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
+                                              __float_as_uint(v1.y));
+                        }
+                        const int n = n0 + c * 32;
+                        if (n < p.N)
+                            store_rows<8>(v, stage, static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 4,
+                                          (size_t)p.N * 4, nrows, (p.N - n) * 4, lane);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kCols / 64; ++c) {
+                        const int n = n0 + c * 64;
+                        if (n < p.N)
+                            store_bf16x64(acc + c * 32, stage,
+                                          static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 2,
+                                          (size_t)p.N * 2, nrows, (p.N - n) * 2, lane);
+                    }
                 }
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
-        const size_t row = (size_t)row0 + r;
-        if constexpr (kGated) {
-            const int I = p.N / 2;
-            float v[8], amax = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                v[k] = acc[0][i][k] * sigmoid(acc[0][i][k]) * acc[1][i][k];
-                amax = fmaxf(amax, fabsf(v[k]));
-            }
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            if (r >= nvalid) continue;
-            amax = quant_amax(amax);
-            const float inv = quant_inverse(amax);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int n = n0 + tx + 16 * k;
-                p.q[row * I + n] = (unsigned char)(pack_e4m3x4(__fmul_rn(v[k], inv), 0.f, 0.f, 0.f) & 0xffu);
-                if (p.h) {
-                    p.h[row * p.N + n] = __float2bfloat16_rn(acc[0][i][k]);
-                    p.h[row * p.N + I + n] = __float2bfloat16_rn(acc[1][i][k]);
-                }
-            }
-            if (tx == 0) p.q_scale[row * (I / 128) + blockIdx.x] = quant_scale(amax);
-        } else {
-            if (r >= nvalid) continue;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int n = n0 + tx + 16 * k;
-                if (n >= p.N) continue;
-                if (p.out_f32) static_cast<float *>(p.out)[row * p.N + n] = acc[0][i][k];
-                else static_cast<__nv_bfloat16 *>(p.out)[row * p.N + n] = __float2bfloat16_rn(acc[0][i][k]);
-            }
-        }
-    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    if (warp == 2) tmem_free<kTmemColumns>(tmem);
 }
 
-static cudaError_t launch_product(const ProductArgs &p, bool gated, cudaStream_t stream) {
-    const long long mtiles = (p.rows + kTileM - 1) / kTileM + p.E;
-    const int ntiles = ((gated ? p.N / 2 : p.N) + kTileN - 1) / kTileN;
-    const dim3 grid((unsigned)ntiles, (unsigned)mtiles);
-    if (gated) expert_product_kernel<true><<<grid, 256, 0, stream>>>(p);
-    else expert_product_kernel<false><<<grid, 256, 0, stream>>>(p);
+// ------------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiled encode_tiled() {
+    static std::atomic<EncodeTiled> fn{nullptr};
+    EncodeTiled f = fn.load(std::memory_order_acquire);
+    if (!f) {
+        void *sym = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        f = reinterpret_cast<EncodeTiled>(sym);
+        fn.store(f, std::memory_order_release);
+    }
+    return f;
+}
+
+// Byte tensor of up to 3 dimensions (x innermost, dense), boxes of 128 x ny (x 1), 128-byte swizzle.
+static bool encode_bytes(CUtensorMap *map, const void *base, uint64_t x, uint64_t y, uint64_t z, int ny) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const int rank = z ? 3 : 2;
+    const cuuint64_t dims[3] = {x, y, z};
+    const cuuint64_t strides[2] = {x, x * y};
+    const cuuint32_t box[3] = {128, (cuuint32_t)ny, 1}, elem[3] = {1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), dims, strides, box, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kBN, bool kTransposed, bool kGated>
+static cudaError_t launch_tiles(const CUtensorMap &map_a, const CUtensorMap &map_w, ProductArgs p,
+                                cudaStream_t stream) {
+    auto kernel = expert_product_kernel<kBN, kTransposed, kGated>;
+    constexpr int smem = ProductLayout<kBN>::kBytes;
+    static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    const int cols = kGated ? kBN / 2 : kBN;
+    p.ntiles = ((kGated ? p.N / 2 : p.N) + cols - 1) / cols;
+    const long long most = ((long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E)) * p.ntiles;
+    const int sms = device_sm_count();
+    const int grid = (int)(most < sms ? (most > 0 ? most : 1) : sms);
+    kernel<<<grid, kProductThreads, smem, stream>>>(map_a, map_w, p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_expert_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
                                const int32_t *expert_offsets, int E, int N, int C, long long rows, bool transpose,
                                bool out_f32, void *out, cudaStream_t stream) {
-    ProductArgs p = {static_cast<const unsigned char *>(a), static_cast<const unsigned char *>(w), a_scale, w_scale,
-                     expert_offsets, E, N, C, rows, transpose, out_f32, out, nullptr, nullptr, nullptr};
-    return launch_product(p, false, stream);
+    CUtensorMap map_a, map_w;
+    if (!encode_bytes(&map_a, a, C, rows, 0, kRowGroup) ||
+        !encode_bytes(&map_w, w, transpose ? N : C, transpose ? C : N, E, 128))
+        return cudaErrorInvalidValue;
+    ProductArgs p = {};
+    p.a_scale = a_scale, p.w_scale = w_scale, p.expert_offsets = expert_offsets;
+    p.E = E, p.N = N, p.C = C, p.rows = (int)rows;
+    p.out_f32 = out_f32, p.out = out;
+    // 256 columns halve the reads of A from shared memory per product; few rows leave more tiles
+    // to spread over the SMs with 128
+    const bool wide = rows >= (long long)E * 64;
+    if (transpose)
+        return wide ? launch_tiles<256, true, false>(map_a, map_w, p, stream)
+                    : launch_tiles<128, true, false>(map_a, map_w, p, stream);
+    return wide ? launch_tiles<256, false, false>(map_a, map_w, p, stream)
+                : launch_tiles<128, false, false>(map_a, map_w, p, stream);
 }
 
 cudaError_t launch_expert_gated_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
                                      const int32_t *expert_offsets, int E, int I, int C, long long rows, void *q,
                                      float *q_scale, void *h, cudaStream_t stream) {
-    ProductArgs p = {static_cast<const unsigned char *>(a), static_cast<const unsigned char *>(w), a_scale, w_scale,
-                     expert_offsets, E, 2 * I, C, rows, false, false, nullptr, static_cast<unsigned char *>(q),
-                     q_scale, static_cast<__nv_bfloat16 *>(h)};
-    return launch_product(p, true, stream);
+    CUtensorMap map_a, map_w;
+    if (!encode_bytes(&map_a, a, C, rows, 0, kRowGroup) || !encode_bytes(&map_w, w, C, 2ull * I, E, 128))
+        return cudaErrorInvalidValue;
+    ProductArgs p = {};
+    p.a_scale = a_scale, p.w_scale = w_scale, p.expert_offsets = expert_offsets;
+    p.E = E, p.N = 2 * I, p.C = C, p.rows = (int)rows;
+    p.q = static_cast<unsigned char *>(q), p.q_scale = q_scale, p.h = static_cast<__nv_bfloat16 *>(h);
+    return launch_tiles<256, false, true>(map_a, map_w, p, stream);
+}
+
+cudaError_t read_product_error(int32_t *host_code, cudaStream_t stream) {
+    int32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_product_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return e;
+    *host_code = v;
+    if (v) {
+        const int32_t zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_product_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    }
+    return e;
 }
 
 }  // namespace moe

@@ -74,6 +74,8 @@ cudaError_t launch_expert_gemm(const void *a, const float *a_scale, const void *
 cudaError_t launch_expert_gated_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
                                      const int32_t *expert_offsets, int E, int I, int C, long long rows, void *q,
                                      float *q_scale, void *h, cudaStream_t stream);
+// Reads and clears the expert products' error word (synchronous).
+cudaError_t read_product_error(int32_t *host_code, cudaStream_t stream);
 cudaError_t launch_gated_backward(const void *h, const void *dv, long long rows, int I, bool fp8, void *dh,
                                   float *dh_scale, cudaStream_t stream);
 cudaError_t launch_combine_backward(const void *dout, const void *y, const int32_t *tok2row, const float *topk_w,

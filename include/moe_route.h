@@ -23,8 +23,8 @@
  *   - Pointers marked "device" are CUDA device (global) memory on the current
  *     device; pointers marked "host" are ordinary host memory read during the
  *     call.  The caller allocates and owns every buffer; the library never
- *     allocates, frees or synchronises (except moe_get_device_error, which
- *     says so).  Work is enqueued on `stream` and runs asynchronously, and
+ *     allocates, frees or synchronises (except moe_get_device_error and
+ *     moe_get_expert_error, which say so).  Work is enqueued on `stream` and runs asynchronously, and
  *     the calls take no host-device synchronisation.  A layer of
  *     moe_route_topk, moe_dispatch (or moe_dispatch_ll[_unordered]),
  *     moe_expert_scale and moe_combine (or moe_combine_ll) can therefore be
@@ -535,6 +535,17 @@ MOE_API moe_status moe_expert_gemm(const void *a, const float *a_scale, const vo
 MOE_API moe_status moe_expert_gated_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
                                          const int32_t *expert_offsets, int E, int I, int C, int rows, void *q,
                                          float *q_scale, void *h, moe_stream_t stream);
+
+/*
+ * moe_get_expert_error -- SYNCHRONOUS: waits for `stream`, then copies to
+ * *host_code and clears the current device's error word of the two products
+ * above: MOE_DEVERR_COPY_TIMEOUT once a bounded wait inside one of their
+ * kernels has run out (the kernel then returns with its output unspecified),
+ * else 0.  Returns MOE_ERR_TIMEOUT, or MOE_OK (MOE_ERR_CUDA if the copy fails,
+ * MOE_ERR_INVALID_ARG for a NULL pointer).  The word is the library's own, one
+ * per device, so the products need no workspace.
+ */
+MOE_API moe_status moe_get_expert_error(int32_t *host_code, moe_stream_t stream);
 
 /*
  * moe_expert_gated_backward -- gradient of the gate.  With (g, u) the halves of

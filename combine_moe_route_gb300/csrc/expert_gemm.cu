@@ -11,16 +11,18 @@
 //
 // A persistent block per SM walks output tiles of 128 rows of one expert x kBN
 // columns.  Its warps have fixed jobs:
-//   warp 0      loads the e4m3 tiles of both operands, 128 channels a stage,
+//   warp 8      loads the e4m3 tiles of both operands, 128 channels a stage,
 //               with tiled bulk tensor copies into a ring of stages;
-//   warp 1      issues the products of a stage (4 x K = 32) into one of the
+//   warp 9      issues the products of a stage (4 x K = 32) into one of the
 //               tensor memory's accumulators, which alternate stage by stage;
-//   warps 4-11  (two warpgroups) read a finished accumulator, one row per
+//   warps 0-7   (two warpgroups) read a finished accumulator, one row per
 //               thread and kBN / 2 columns per warpgroup, scale it into
 //               registers, and after the last stage write the tile.
-// A row tile that is not full loads only the groups of 32 rows it has; rows of
-// an accumulator past them hold leftovers that nothing reads (a row of the
-// result depends on its own row of A alone).
+// A row tile is one load of 128 rows, or of 32 where it has no more: a block's
+// loads take about 165 cycles each to issue, so a stage has as few of them as
+// its operands allow.  Rows past a tile's own are the next expert's, or hold
+// leftovers; nothing reads them (a row of the result depends on its own row of
+// A alone).
 //
 // The forward weight [E, N, C] is a K-major operand.  The transposed product
 // reads the same weight, [E, C, N] in its terms, as an MN-major operand, so
@@ -39,12 +41,16 @@
 namespace moe {
 
 constexpr int kProductThreads = 384;
+// Registers of a thread of the loading and issuing warpgroup and of the two
+// others, out of the 168 that a block of 384 threads starts with:
+// 88 + 2 * 208 = 3 * 168.
+constexpr int kIssueRegisters = 88, kSumRegisters = 208;
 constexpr int kRowTile = 128;     // rows of a tile: the M of one product
-constexpr int kRowGroup = 32;     // rows per load of A
+constexpr int kFewRows = 32;      // rows of the small load of A
 constexpr int kBlockK = 128;      // channels per stage: one scale block, 128 bytes
 constexpr int kStageA = kRowTile * kBlockK;
-constexpr int kWeightBox = 128 * kBlockK;   // bytes of one load of the weight: 128 columns x 128 channels
 constexpr int kTmemColumns = 512;
+constexpr int kChunk = 16;                  // accumulator columns read at a time
 constexpr int kStagingWarp = 16 * 128;      // output staging of a warp: 16 rows x 128 bytes
 
 // Set when a bounded wait of a product kernel ran out (never in a sound run).
@@ -63,19 +69,33 @@ struct ProductArgs {
     __nv_bfloat16 *h;   // gated form: [rows, N] or null
 };
 
-template <int kBN>
+// kCtas blocks work on one tile of kCtas * 128 rows x kBN columns.
+template <int kCtas, int kBN>
 struct ProductLayout {
-    static constexpr int kStageBytes = kStageA + kBN * kBlockK;
+    static constexpr int kStageBytes = kStageA + kBN / kCtas * kBlockK;
     static constexpr int kStages = 192 * 1024 / kStageBytes;
     static constexpr int kBuffers = kTmemColumns / kBN;
     static constexpr int kStaging = kStages * kStageBytes;
     static constexpr int kBytes = kStaging + 8 * kStagingWarp + 1024;   // + alignment of the swizzled tiles
 };
 
-template <int kBN>
+// Columns of one load of the weight.  A block's share of a stage is one load,
+// or two of 128: an MN-major row is 128 bytes (the swizzle's span), and the
+// gate's and the up projection's columns lie apart.
+template <int kCtas, int kBN, bool kTransposed, bool kGated>
+constexpr int weight_box() {
+    return (kTransposed || kGated) ? 128 : kBN / kCtas;
+}
+
+// Bytes that a row tile's load of A brings.
+__device__ __forceinline__ uint32_t row_load_bytes(int valid) {
+    return valid > kFewRows ? kRowTile * kBlockK : valid > 0 ? kFewRows * kBlockK : 0;
+}
+
+template <int kCtas, int kBN>
 struct ProductShared {
-    uint64_t full[ProductLayout<kBN>::kStages], empty[ProductLayout<kBN>::kStages];
-    uint64_t acc_full[ProductLayout<kBN>::kBuffers], acc_empty[ProductLayout<kBN>::kBuffers];
+    uint64_t full[ProductLayout<kCtas, kBN>::kStages], empty[ProductLayout<kCtas, kBN>::kStages];
+    uint64_t acc_full[ProductLayout<kCtas, kBN>::kBuffers], acc_empty[ProductLayout<kCtas, kBN>::kBuffers];
     uint64_t pair[4];                      // gated: the two warps that share a quarter of the rows
     uint64_t drain;
     uint32_t tmem;
@@ -86,13 +106,18 @@ struct ProductShared {
 };
 
 // Wait for a barrier's phase; false once any wait of the block has run out.
+// The clock is read once per kPolls polls only: reading %globaltimer on every
+// wait that did not succeed at once cost more than the rest of a stage.
+constexpr uint32_t kPolls = 256;
 template <class Shared>
 __device__ __forceinline__ bool wait_or_stop(Shared &s, uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if (i % kPolls != 0) continue;
         if (s.stop) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
             s.stop = 1;
             atomicOr(&g_product_error, MOE_DEVERR_COPY_TIMEOUT);
             return false;
@@ -114,7 +139,8 @@ struct Ring {
 };
 
 struct Tile {
-    int e, row0, valid, n;   // expert, first row, rows, column tile
+    int e, row0, valid, n;   // expert, this block's first row and rows, column tile
+    int pair_valid;          // rows of the blocks together
 };
 
 // Expert e's first row and number of rows, inside [0, rows] whatever the offsets hold.
@@ -126,14 +152,15 @@ __device__ __forceinline__ int2 expert_rows(const ProductArgs &p, int e) {
 
 // Tile t: experts in order; within an expert the row tiles of one column tile
 // come first, so that blocks working at the same time share the weight.
-template <class Shared>
-__device__ __forceinline__ Tile tile_at(const Shared &s, const ProductArgs &p, long long t) {
+template <int kCtas, class Shared>
+__device__ __forceinline__ Tile tile_at(const Shared &s, const ProductArgs &p, long long t, int rank) {
     const int e = upper_bound_minus_one(s.tiles, p.E, (int)(t / p.ntiles));
     const int mt = s.tiles[e + 1] - s.tiles[e];
     const int i = (int)(t - (long long)s.tiles[e] * p.ntiles);
     const int m = i % mt;
     const int2 r = expert_rows(p, e);
-    return {e, r.x + m * kRowTile, min(r.y - m * kRowTile, kRowTile), i / mt};
+    const int valid = min(r.y - m * (kCtas * kRowTile), kCtas * kRowTile);
+    return {e, r.x + (m * kCtas + rank) * kRowTile, max(min(valid - rank * kRowTile, kRowTile), 0), i / mt, valid};
 }
 
 // Writes the 16-byte chunks a lane holds of its row (32 rows of a warp, kChunks
@@ -175,15 +202,31 @@ __device__ __forceinline__ void store_bf16x64(const float2 *acc, unsigned char *
     store_rows<8>(v, stage, dst, pitch, nrows, limit, lane);
 }
 
-template <int kBN, bool kTransposed, bool kGated>
+// Columns of a product at the right edge, where `left` are left.  Both blocks of
+// a pair bring half of them, and half a tile's columns have to be a multiple of 16
+// for the loads of an MN-major weight (columns past N read as zeros).
+template <int kCtas, int kBN>
+__device__ __forceinline__ int tile_columns(int left) {
+    const int cols = min(kBN, left);
+    return kCtas == 2 ? (cols + 31) & ~31 : cols;
+}
+
+// The accumulator column of a warpgroup's i-th column.
+template <int kCols, bool kGated>
+__device__ __forceinline__ int chunk_column(int wg, int i) {
+    return kGated ? (i < 64 ? wg * 64 + i : 128 + wg * 64 + (i - 64)) : wg * kCols + i;
+}
+
+template <int kCtas, int kBN, bool kTransposed, bool kGated>
 __global__ void __launch_bounds__(kProductThreads, 1)
-    expert_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                          const ProductArgs p) {
-    using Layout = ProductLayout<kBN>;
+    expert_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_few,
+                          const __grid_constant__ CUtensorMap map_w, const ProductArgs p) {
+    using Layout = ProductLayout<kCtas, kBN>;
     extern __shared__ unsigned char s_raw[];
-    __shared__ ProductShared<kBN> s;
+    __shared__ ProductShared<kCtas, kBN> s;
     unsigned char *tiles = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);   // swizzled tiles: 1024-byte aligned
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
     const int nkb = (p.C + kBlockK - 1) / kBlockK;
 
     // prologue: barriers, tensor memory, and the experts' row tiles
@@ -194,16 +237,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
         for (int i = 0; i < Layout::kBuffers; ++i) {
             mbar_init(&s.acc_full[i], 1);
-            mbar_init(&s.acc_empty[i], 8);
+            mbar_init(&s.acc_empty[i], 8 * kCtas);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&s.pair[i], 2);
         mbar_init(&s.drain, 1);
         s.stop = 0;
         fence_mbarrier_init();
         prefetch_tensor_map(&map_a);
+        prefetch_tensor_map(&map_few);
         prefetch_tensor_map(&map_w);
     }
-    if (warp == 2) tmem_alloc<kTmemColumns>(&s.tmem);
+    if (warp == 9) tmem_alloc<kCtas, kTmemColumns>(&s.tmem);
     {
         constexpr int kPer = (MOE_MAX_EXPERTS + kProductThreads - 1) / kProductThreads;
         int mine = 0, mt[kPer];
@@ -211,7 +255,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         for (int i = 0; i < kPer; ++i) {
             const int e = threadIdx.x * kPer + i;
             mt[i] = 0;
-            if (e < p.E) mt[i] = (expert_rows(p, e).y + kRowTile - 1) / kRowTile;
+            if (e < p.E) mt[i] = (expert_rows(p, e).y + kCtas * kRowTile - 1) / (kCtas * kRowTile);
             mine += mt[i];
         }
         int sum = mine;
@@ -234,36 +278,44 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
     }
     tcgen05_fence_before();
-    __syncthreads();
+    if (kCtas == 2) cluster_barrier();   // the pair's barriers are ready
+    else __syncthreads();
     tcgen05_fence_after();
     const long long total = (long long)s.tiles[p.E] * p.ntiles;
     const uint32_t tmem = s.tmem;
 
-    if (warp < 4) {
-        registers_decrease<40>();
-        if (warp == 0 && lane == 0) {
+    if (warp >= 8) {
+        registers_decrease<kIssueRegisters>();
+        if (warp == 8 && lane == 0) {
             // ---------------------------------------------------- loads
             Ring r;
             long long issued = 0;
             bool go = true;
-            for (long long t = blockIdx.x; go && t < total; t += gridDim.x) {
-                const Tile tile = tile_at(s, p, t);
-                const int groups = (tile.valid + kRowGroup - 1) / kRowGroup;
+            for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
+                const Tile tile = tile_at<kCtas>(s, p, t, rank);
                 const int n0 = tile.n * (kGated ? kBN / 2 : kBN);
-                const int boxes = kGated ? 2 : (min(kBN, p.N - n0) + 127) / 128;
-                const uint32_t bytes = groups * kRowGroup * kBlockK + boxes * kWeightBox;
+                const int cols = kGated ? kBN : tile_columns<kCtas, kBN>(p.N - n0);
+                // a pair splits the columns: each block brings half of them
+                constexpr int kBox = weight_box<kCtas, kBN, kTransposed, kGated>(), kBoxBytes = kBox * kBlockK;
+                const int boxes = kCtas == 2 ? 1 : kGated ? 2 : (cols + kBox - 1) / kBox;
+                const int first = kGated ? n0 + rank * (p.N / 2) : n0 + rank * (cols / 2);
+                const CUtensorMap *rows = tile.valid > kFewRows ? &map_a : &map_few;
+                const uint32_t bytes =
+                    kCtas * boxes * kBoxBytes +
+                    (kCtas == 2 ? row_load_bytes(min(tile.pair_valid, kRowTile)) +
+                                      row_load_bytes(tile.pair_valid - kRowTile)
+                                : row_load_bytes(tile.valid));
                 for (int kb = 0; kb < nkb; ++kb) {
                     if (!(go = wait_or_stop(s, &s.empty[r.slot], r.parity ^ 1u))) break;
                     unsigned char *a = tiles + r.slot * Layout::kStageBytes, *w = a + kStageA;
                     uint64_t *bar = &s.full[r.slot];
-                    mbar_arrive_expect_tx(bar, bytes);
-                    for (int i = 0; i < groups; ++i)
-                        tensor_load_2d(a + i * kRowGroup * kBlockK, &map_a, kb * kBlockK, tile.row0 + i * kRowGroup,
-                                       bar);
+                    if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
+                    if (tile.valid > 0) tensor_load_2d<kCtas>(a, rows, kb * kBlockK, tile.row0, bar);
                     for (int i = 0; i < boxes; ++i) {
-                        const int n = n0 + i * (kGated ? p.N / 2 : 128);
-                        if (kTransposed) tensor_load_3d(w + i * kWeightBox, &map_w, n, kb * kBlockK, tile.e, bar);
-                        else tensor_load_3d(w + i * kWeightBox, &map_w, kb * kBlockK, n, tile.e, bar);
+                        const int n = first + i * (kGated ? p.N / 2 : kBox);
+                        if (kTransposed)
+                            tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, n, kb * kBlockK, tile.e, bar);
+                        else tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, kb * kBlockK, n, tile.e, bar);
                     }
                     r.advance(Layout::kStages);
                     ++issued;
@@ -275,16 +327,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int i = 0; i < last; ++i) {
                 r.slot = (r.slot == 0 ? Layout::kStages : r.slot) - 1;
                 if (r.slot == Layout::kStages - 1) r.parity ^= 1u;
-                if (!wait_or_stop(s, &s.empty[r.slot], r.parity)) mbar_wait_bounded(&s.full[r.slot], r.parity);
+                if (!wait_or_stop(s, &s.empty[r.slot], r.parity) && rank == 0)
+                    mbar_wait_bounded(&s.full[r.slot], r.parity);   // a pair's barrier counts both blocks' loads
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 9 && lane == 0 && rank == 0) {
             // ------------------------------------------------- products
             Ring r, b;
             bool go = true;
-            for (long long t = blockIdx.x; go && t < total; t += gridDim.x) {
-                const Tile tile = tile_at(s, p, t);
-                const int cols = kGated ? kBN : min(kBN, p.N - tile.n * kBN);   // a multiple of 16
-                const uint32_t instruction = f8_instruction(kRowTile, cols, kTransposed);
+            for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
+                const Tile tile = tile_at<kCtas>(s, p, t, rank);
+                const int cols = kGated ? kBN : tile_columns<kCtas, kBN>(p.N - tile.n * kBN);
+                const uint32_t instruction = f8_instruction(kCtas * kRowTile, cols, kTransposed);
                 for (int kb = 0; kb < nkb; ++kb) {
                     if (!(go = wait_or_stop(s, &s.acc_empty[b.slot], b.parity ^ 1u))) break;
                     if (!(go = wait_or_stop(s, &s.full[r.slot], r.parity))) break;
@@ -294,35 +347,35 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     for (int k = 0; k < kBlockK / 32; ++k) {
                         // 32 channels on: 32 bytes along a K-major row, 32 rows of 128 bytes MN-major
                         const uint64_t da = smem_descriptor(a + k * 32, 16, 1024);
-                        const uint64_t dw = kTransposed ? smem_descriptor(w + k * 32 * 128, kWeightBox, 1024)
+                        const uint64_t dw = kTransposed ? smem_descriptor(w + k * 32 * 128, 128 * kBlockK, 1024)
                                                         : smem_descriptor(w + k * 32, 16, 1024);
-                        mma_f8(tmem + b.slot * kBN, da, dw, instruction, k > 0);
+                        mma_f8<kCtas>(tmem + b.slot * kBN, da, dw, instruction, k > 0);
                     }
-                    mma_commit(&s.empty[r.slot]);
-                    mma_commit(&s.acc_full[b.slot]);
+                    mma_commit<kCtas>(&s.empty[r.slot]);
+                    mma_commit<kCtas>(&s.acc_full[b.slot]);
                     r.advance(Layout::kStages);
                     b.advance(Layout::kBuffers);
                 }
             }
             if (!go) {   // leave no product running
-                mma_commit(&s.drain);
+                mma_commit<kCtas>(&s.drain);
                 mbar_wait_bounded(&s.drain, 0);
             }
         }
         __syncwarp();
     } else {
         // ------------------------------------- scaled sums and the output
-        registers_increase<232>();
+        registers_increase<kSumRegisters>();
         constexpr int kCols = kBN / 2;            // columns of a warpgroup
-        const int wg = (warp >> 2) - 1, quarter = warp & 3;
-        unsigned char *stage = tiles + Layout::kStaging + (warp - 4) * kStagingWarp;
+        const int wg = warp >> 2, quarter = warp & 3;
+        unsigned char *stage = tiles + Layout::kStaging + warp * kStagingWarp;
         const int nb = (p.N + 127) / 128;         // scale blocks along the columns
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         Ring b;
         uint32_t pair_parity = 0;
         bool go = true;
-        for (long long t = blockIdx.x; go && t < total; t += gridDim.x) {
-            const Tile tile = tile_at(s, p, t);
+        for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
+            const Tile tile = tile_at<kCtas>(s, p, t, rank);
             const int nrows = min(tile.valid - quarter * 32, 32);   // rows of this warp
             const int n0 = kGated ? tile.n * 128 : tile.n * kBN + wg * kCols;
             const bool active = nrows > 0 && (kGated || n0 < p.N);
@@ -366,23 +419,29 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     if (!go) break;
                     tcgen05_fence_after();
                     if (active) {
+                        // the next columns are on their way while these are added
+                        uint32_t v[2][kChunk];
+                        const uint32_t at = lanes + b.slot * kBN;
+                        tmem_load(at + chunk_column<kCols, kGated>(wg, 0), v[0]);
 #pragma unroll
-                        for (int c = 0; c < kCols / 32; ++c) {
-                            const int col = kGated ? (c < 2 ? wg * 64 + c * 32 : 128 + wg * 64 + (c - 2) * 32)
-                                                   : wg * kCols + c * 32;
-                            const float fc = (kGated && c >= 2) ? g[i] : f[i];
-                            uint32_t v[32];
-                            tmem_load32(lanes + b.slot * kBN + col, v);
+                        for (int c = 0; c < kCols / kChunk; ++c) {
                             tmem_wait_load();
+                            if (c + 1 < kCols / kChunk)
+                                tmem_load(at + chunk_column<kCols, kGated>(wg, (c + 1) * kChunk), v[(c + 1) & 1]);
+                            const float fc = (kGated && c * kChunk >= 64) ? g[i] : f[i];
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                fma_pair(acc[c * 16 + k], make_float2(fc, fc),
-                                         make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+                            for (int k = 0; k < kChunk / 2; ++k)
+                                fma_pair(acc[c * (kChunk / 2) + k], make_float2(fc, fc),
+                                         make_float2(__uint_as_float(v[c & 1][2 * k]),
+                                                     __uint_as_float(v[c & 1][2 * k + 1])));
                         }
                     }
                     tcgen05_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.acc_empty[b.slot]);
+                    if (lane == 0) {
+                        if (kCtas == 2) mbar_arrive_first(&s.acc_empty[b.slot]);
+                        else mbar_arrive(&s.acc_empty[b.slot]);
+                    }
                     b.advance(Layout::kBuffers);
                 }
             }
@@ -459,9 +518,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
     }
     tcgen05_fence_before();
-    __syncthreads();
+    if (kCtas == 2) cluster_barrier();   // nothing of the other block's reaches this one any more
+    else __syncthreads();
     tcgen05_fence_after();
-    if (warp == 2) tmem_free<kTmemColumns>(tmem);
+    if (warp == 9) tmem_free<kCtas, kTmemColumns>(tmem);
 }
 
 // ------------------------------------------------------------------- host
@@ -498,11 +558,15 @@ static bool encode_bytes(CUtensorMap *map, const void *base, uint64_t x, uint64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kBN, bool kTransposed, bool kGated>
-static cudaError_t launch_tiles(const CUtensorMap &map_a, const CUtensorMap &map_w, ProductArgs p,
-                                cudaStream_t stream) {
-    auto kernel = expert_product_kernel<kBN, kTransposed, kGated>;
-    constexpr int smem = ProductLayout<kBN>::kBytes;
+template <int kCtas, int kBN, bool kTransposed, bool kGated>
+static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cudaStream_t stream) {
+    CUtensorMap map_a, map_few, map_w;
+    if (!encode_bytes(&map_a, a, p.C, p.rows, 0, kRowTile) || !encode_bytes(&map_few, a, p.C, p.rows, 0, kFewRows) ||
+        !encode_bytes(&map_w, w, kTransposed ? p.N : p.C, kTransposed ? p.C : p.N, p.E,
+                      kTransposed ? kBlockK : weight_box<kCtas, kBN, kTransposed, kGated>()))
+        return cudaErrorInvalidValue;
+    auto kernel = expert_product_kernel<kCtas, kBN, kTransposed, kGated>;
+    constexpr int smem = ProductLayout<kCtas, kBN>::kBytes;
     static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -515,45 +579,49 @@ static cudaError_t launch_tiles(const CUtensorMap &map_a, const CUtensorMap &map
     }
     const int cols = kGated ? kBN / 2 : kBN;
     p.ntiles = ((kGated ? p.N / 2 : p.N) + cols - 1) / cols;
-    const long long most = ((long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E)) * p.ntiles;
-    const int sms = device_sm_count();
-    const int grid = (int)(most < sms ? (most > 0 ? most : 1) : sms);
-    kernel<<<grid, kProductThreads, smem, stream>>>(map_a, map_w, p);
-    return cudaGetLastError();
+    // no more tiles than this exist; the blocks walk them
+    const long long most = ((long long)p.rows / (kCtas * kRowTile) + (p.rows < p.E ? p.rows : p.E)) * p.ntiles;
+    const int groups = device_sm_count() / kCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(kCtas * (most < groups ? (most > 0 ? most : 1) : groups)));
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_few, map_w, p);
+}
+
+template <bool kTransposed, bool kGated>
+static cudaError_t launch_product(const void *a, const void *w, const ProductArgs &p, cudaStream_t stream) {
+    const bool pairs = p.rows >= (long long)p.E * 192;
+    if (pairs) return launch_tiles<2, 256, kTransposed, kGated>(a, w, p, stream);
+    if constexpr (kGated) return launch_tiles<1, 256, kTransposed, kGated>(a, w, p, stream);
+    else return launch_tiles<1, 128, kTransposed, kGated>(a, w, p, stream);
 }
 
 cudaError_t launch_expert_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
                                const int32_t *expert_offsets, int E, int N, int C, long long rows, bool transpose,
                                bool out_f32, void *out, cudaStream_t stream) {
-    CUtensorMap map_a, map_w;
-    if (!encode_bytes(&map_a, a, C, rows, 0, kRowGroup) ||
-        !encode_bytes(&map_w, w, transpose ? N : C, transpose ? C : N, E, 128))
-        return cudaErrorInvalidValue;
     ProductArgs p = {};
     p.a_scale = a_scale, p.w_scale = w_scale, p.expert_offsets = expert_offsets;
     p.E = E, p.N = N, p.C = C, p.rows = (int)rows;
     p.out_f32 = out_f32, p.out = out;
-    // 256 columns halve the reads of A from shared memory per product; few rows leave more tiles
-    // to spread over the SMs with 128
-    const bool wide = rows >= (long long)E * 64;
-    if (transpose)
-        return wide ? launch_tiles<256, true, false>(map_a, map_w, p, stream)
-                    : launch_tiles<128, true, false>(map_a, map_w, p, stream);
-    return wide ? launch_tiles<256, false, false>(map_a, map_w, p, stream)
-                : launch_tiles<128, false, false>(map_a, map_w, p, stream);
+    return transpose ? launch_product<true, false>(a, w, p, stream) : launch_product<false, false>(a, w, p, stream);
 }
 
 cudaError_t launch_expert_gated_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
                                      const int32_t *expert_offsets, int E, int I, int C, long long rows, void *q,
                                      float *q_scale, void *h, cudaStream_t stream) {
-    CUtensorMap map_a, map_w;
-    if (!encode_bytes(&map_a, a, C, rows, 0, kRowGroup) || !encode_bytes(&map_w, w, C, 2ull * I, E, 128))
-        return cudaErrorInvalidValue;
     ProductArgs p = {};
     p.a_scale = a_scale, p.w_scale = w_scale, p.expert_offsets = expert_offsets;
     p.E = E, p.N = 2 * I, p.C = C, p.rows = (int)rows;
     p.q = static_cast<unsigned char *>(q), p.q_scale = q_scale, p.h = static_cast<__nv_bfloat16 *>(h);
-    return launch_tiles<256, false, true>(map_a, map_w, p, stream);
+    return launch_product<false, true>(a, w, p, stream);
 }
 
 cudaError_t read_product_error(int32_t *host_code, cudaStream_t stream) {

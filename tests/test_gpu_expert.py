@@ -16,6 +16,8 @@ COUNTS = {
     "tile_edges": [127, 128, 129, 0, 1, 255, 257],
     "small": [5, 0, 31, 33, 2, 64, 65, 0],
     "skewed": [700, 1, 0, 3, 90, 0, 0, 12],
+    "full": [256, 257, 255, 511, 0, 700],
+    "one_full": [385],
 }
 
 

@@ -13,8 +13,11 @@
 // columns.  Its warps have fixed jobs:
 //   warp 8      loads the e4m3 tiles of both operands, 128 channels a stage,
 //               with tiled bulk tensor copies into a ring of stages;
-//   warp 9      issues the products of a stage (4 x K = 32) into one of the
-//               tensor memory's accumulators, which alternate stage by stage;
+//   warps 9, 10 issue the products of a stage (4 x K = 32 each, 128 columns)
+//               into the tensor memory's accumulators, four in turn;
+//   warp 11     forms the products of the two scales, one per row, channel block
+//               and half of the columns, some blocks ahead, in a ring of its own
+//               (reading them where they are used stalled the sums on L2);
 //   warps 0-7   (two warpgroups) read a finished accumulator, one row per
 //               thread and kBN / 2 columns per warpgroup, scale it into
 //               registers, and after the last stage write the tile.
@@ -43,14 +46,14 @@ namespace moe {
 constexpr int kProductThreads = 384;
 // Registers of a thread of the loading and issuing warpgroup and of the two
 // others, out of the 168 that a block of 384 threads starts with:
-// 88 + 2 * 208 = 3 * 168.
-constexpr int kIssueRegisters = 88, kSumRegisters = 208;
+// 56 + 2 * 224 = 3 * 168.
+constexpr int kIssueRegisters = 56, kSumRegisters = 224;
 constexpr int kRowTile = 128;     // rows of a tile: the M of one product
 constexpr int kFewRows = 32;      // rows of the small load of A
 constexpr int kBlockK = 128;      // channels per stage: one scale block, 128 bytes
 constexpr int kStageA = kRowTile * kBlockK;
+constexpr int kScaleSlots = 4;             // of the ring of scales
 constexpr int kTmemColumns = 512;
-constexpr int kChunk = 16;                  // accumulator columns read at a time
 constexpr int kStagingWarp = 16 * 128;      // output staging of a warp: 16 rows x 128 bytes
 
 // Set when a bounded wait of a product kernel ran out (never in a sound run).
@@ -69,22 +72,28 @@ struct ProductArgs {
     __nv_bfloat16 *h;   // gated form: [rows, N] or null
 };
 
-// kCtas blocks work on one tile of kCtas * 128 rows x kBN columns.
+// kCtas blocks work on one tile of kCtas * 128 rows x kBN columns.  A stage's
+// product is done 128 columns at a time (kHalves units), each into an
+// accumulator of its own: four accumulators keep the tensor cores busy across
+// the round trip accumulator -> sums -> accumulator free, about 1300 cycles
+// with a unit's product itself, which two of 256 columns did not.
 template <int kCtas, int kBN>
 struct ProductLayout {
+    static constexpr int kHalves = kBN / 128;
     static constexpr int kStageBytes = kStageA + kBN / kCtas * kBlockK;
     static constexpr int kStages = 192 * 1024 / kStageBytes;
-    static constexpr int kBuffers = kTmemColumns / kBN;
+    static constexpr int kBuffers = kTmemColumns / 128;
+    static constexpr int kGroup = kBuffers / kHalves;   // stages that fill every accumulator once
     static constexpr int kStaging = kStages * kStageBytes;
     static constexpr int kBytes = kStaging + 8 * kStagingWarp + 1024;   // + alignment of the swizzled tiles
 };
 
 // Columns of one load of the weight.  A block's share of a stage is one load,
-// or two of 128: an MN-major row is 128 bytes (the swizzle's span), and the
-// gate's and the up projection's columns lie apart.
+// or two: an MN-major row is 128 bytes (the swizzle's span), and the gate's and
+// the up projection's columns lie apart.
 template <int kCtas, int kBN, bool kTransposed, bool kGated>
 constexpr int weight_box() {
-    return (kTransposed || kGated) ? 128 : kBN / kCtas;
+    return kGated ? 128 / kCtas : kTransposed ? 128 : kBN / kCtas;
 }
 
 // Bytes that a row tile's load of A brings.
@@ -97,34 +106,14 @@ struct ProductShared {
     uint64_t full[ProductLayout<kCtas, kBN>::kStages], empty[ProductLayout<kCtas, kBN>::kStages];
     uint64_t acc_full[ProductLayout<kCtas, kBN>::kBuffers], acc_empty[ProductLayout<kCtas, kBN>::kBuffers];
     uint64_t pair[4];                      // gated: the two warps that share a quarter of the rows
-    uint64_t drain;
+    uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
+    uint64_t drain[2];
     uint32_t tmem;
-    volatile int32_t stop;                 // a wait ran out: every role leaves
     int32_t warp_tiles[kProductThreads / 32];
     int32_t tiles[MOE_MAX_EXPERTS + 1];    // row tiles before expert e
+    float scales[kScaleSlots][ProductLayout<kCtas, kBN>::kBuffers][kRowTile];   // a_scale * w_scale of a group
     float amax[2][2][kRowTile];            // gated: by tile parity, each warpgroup's maximum of a row's block
 };
-
-// Wait for a barrier's phase; false once any wait of the block has run out.
-// The clock is read once per kPolls polls only: reading %globaltimer on every
-// wait that did not succeed at once cost more than the rest of a stage.
-constexpr uint32_t kPolls = 256;
-template <class Shared>
-__device__ __forceinline__ bool wait_or_stop(Shared &s, uint64_t *bar, uint32_t parity) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if (i % kPolls != 0) continue;
-        if (s.stop) return false;
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitLimitNs) {
-            s.stop = 1;
-            atomicOr(&g_product_error, MOE_DEVERR_COPY_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
 
 // Position in a ring of n slots and the parity of its current pass.
 struct Ring {
@@ -202,21 +191,6 @@ __device__ __forceinline__ void store_bf16x64(const float2 *acc, unsigned char *
     store_rows<8>(v, stage, dst, pitch, nrows, limit, lane);
 }
 
-// Columns of a product at the right edge, where `left` are left.  Both blocks of
-// a pair bring half of them, and half a tile's columns have to be a multiple of 16
-// for the loads of an MN-major weight (columns past N read as zeros).
-template <int kCtas, int kBN>
-__device__ __forceinline__ int tile_columns(int left) {
-    const int cols = min(kBN, left);
-    return kCtas == 2 ? (cols + 31) & ~31 : cols;
-}
-
-// The accumulator column of a warpgroup's i-th column.
-template <int kCols, bool kGated>
-__device__ __forceinline__ int chunk_column(int wg, int i) {
-    return kGated ? (i < 64 ? wg * 64 + i : 128 + wg * 64 + (i - 64)) : wg * kCols + i;
-}
-
 template <int kCtas, int kBN, bool kTransposed, bool kGated>
 __global__ void __launch_bounds__(kProductThreads, 1)
     expert_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_few,
@@ -225,7 +199,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     extern __shared__ unsigned char s_raw[];
     __shared__ ProductShared<kCtas, kBN> s;
     unsigned char *tiles = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);   // swizzled tiles: 1024-byte aligned
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // broadcast, so that the compiler knows it to be the same in a warp
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const bool issue = lane == 0;
     const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
     const int nkb = (p.C + kBlockK - 1) / kBlockK;
 
@@ -233,15 +209,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < Layout::kStages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
+            mbar_init(&s.empty[i], Layout::kHalves);
         }
         for (int i = 0; i < Layout::kBuffers; ++i) {
             mbar_init(&s.acc_full[i], 1);
             mbar_init(&s.acc_empty[i], 8 * kCtas);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&s.pair[i], 2);
-        mbar_init(&s.drain, 1);
-        s.stop = 0;
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(&s.scale_full[i], 1);
+            mbar_init(&s.scale_empty[i], 8);
+        }
+        mbar_init(&s.drain[0], 1);
+        mbar_init(&s.drain[1], 1);
         fence_mbarrier_init();
         prefetch_tensor_map(&map_a);
         prefetch_tensor_map(&map_few);
@@ -284,38 +264,44 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const long long total = (long long)s.tiles[p.E] * p.ntiles;
     const uint32_t tmem = s.tmem;
 
+    // Every wait below has a limit and runs out on its own if its partner has left; a role whose
+    // wait ran out leaves its loop.  `go` is looked at after the work that a wait released is
+    // issued: that work is harmless on stale data, and the look is then off the critical path.
+    const auto at = [](const uint64_t *bar) { return smem_u32(bar); };
+    const uint32_t tiles_at = smem_u32(tiles);
+    bool go = true;
     if (warp >= 8) {
         registers_decrease<kIssueRegisters>();
-        if (warp == 8 && lane == 0) {
+        if (warp == 8) {
             // ---------------------------------------------------- loads
             Ring r;
             long long issued = 0;
-            bool go = true;
             for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
                 const Tile tile = tile_at<kCtas>(s, p, t, rank);
                 const int n0 = tile.n * (kGated ? kBN / 2 : kBN);
-                const int cols = kGated ? kBN : tile_columns<kCtas, kBN>(p.N - n0);
                 // a pair splits the columns: each block brings half of them
                 constexpr int kBox = weight_box<kCtas, kBN, kTransposed, kGated>(), kBoxBytes = kBox * kBlockK;
-                const int boxes = kCtas == 2 ? 1 : kGated ? 2 : (cols + kBox - 1) / kBox;
-                const int first = kGated ? n0 + rank * (p.N / 2) : n0 + rank * (cols / 2);
+                constexpr int kBoxes = kBN / kCtas / kBox;
+                const int first = n0 + rank * (kGated ? 64 : 128);
                 const CUtensorMap *rows = tile.valid > kFewRows ? &map_a : &map_few;
                 const uint32_t bytes =
-                    kCtas * boxes * kBoxBytes +
+                    kCtas * kBoxes * kBoxBytes +
                     (kCtas == 2 ? row_load_bytes(min(tile.pair_valid, kRowTile)) +
                                       row_load_bytes(tile.pair_valid - kRowTile)
                                 : row_load_bytes(tile.valid));
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!(go = wait_or_stop(s, &s.empty[r.slot], r.parity ^ 1u))) break;
-                    unsigned char *a = tiles + r.slot * Layout::kStageBytes, *w = a + kStageA;
-                    uint64_t *bar = &s.full[r.slot];
-                    if (rank == 0) mbar_arrive_expect_tx(bar, bytes);
-                    if (tile.valid > 0) tensor_load_2d<kCtas>(a, rows, kb * kBlockK, tile.row0, bar);
-                    for (int i = 0; i < boxes; ++i) {
+                    go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.empty[r.slot]), r.parity ^ 1u));
+                    if (!go) break;
+                    const uint32_t a = tiles_at + r.slot * Layout::kStageBytes, w = a + kStageA;
+                    const uint32_t bar = at(&s.full[r.slot]);
+                    mbar_expect(bar, bytes, issue && rank == 0);
+                    tensor_load_2d<kCtas>(a, rows, kb * kBlockK, tile.row0, bar, issue && tile.valid > 0);
+#pragma unroll
+                    for (int i = 0; i < kBoxes; ++i) {
                         const int n = first + i * (kGated ? p.N / 2 : kBox);
                         if (kTransposed)
-                            tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, n, kb * kBlockK, tile.e, bar);
-                        else tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, kb * kBlockK, n, tile.e, bar);
+                            tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, n, kb * kBlockK, tile.e, bar, issue);
+                        else tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, kb * kBlockK, n, tile.e, bar, issue);
                     }
                     r.advance(Layout::kStages);
                     ++issued;
@@ -327,128 +313,161 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int i = 0; i < last; ++i) {
                 r.slot = (r.slot == 0 ? Layout::kStages : r.slot) - 1;
                 if (r.slot == Layout::kStages - 1) r.parity ^= 1u;
-                if (!wait_or_stop(s, &s.empty[r.slot], r.parity) && rank == 0)
-                    mbar_wait_bounded(&s.full[r.slot], r.parity);   // a pair's barrier counts both blocks' loads
+                go = go && __all_sync(0xffffffffu, mbar_wait_polls(at(&s.empty[r.slot]), r.parity));
+                if (!go && rank == 0)   // a pair's barrier counts both blocks' loads
+                    mbar_wait_polls(at(&s.full[r.slot]), r.parity);
             }
-        } else if (warp == 9 && lane == 0 && rank == 0) {
+        } else if (warp < 9 + Layout::kHalves) {
             // ------------------------------------------------- products
-            Ring r, b;
-            bool go = true;
-            for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
-                const Tile tile = tile_at<kCtas>(s, p, t, rank);
-                const int cols = kGated ? kBN : tile_columns<kCtas, kBN>(p.N - tile.n * kBN);
-                const uint32_t instruction = f8_instruction(kCtas * kRowTile, cols, kTransposed);
-                for (int kb = 0; kb < nkb; ++kb) {
-                    if (!(go = wait_or_stop(s, &s.acc_empty[b.slot], b.parity ^ 1u))) break;
-                    if (!(go = wait_or_stop(s, &s.full[r.slot], r.parity))) break;
-                    tcgen05_fence_after();
-                    const uint32_t a = smem_u32(tiles) + r.slot * Layout::kStageBytes, w = a + kStageA;
+            // one warp per half: a thread issues about as fast as its products run, so one alone
+            // would leave the tensor cores idle while it waits on barriers
+            if (rank == 0) {
+                const int half = warp - 9;
+                constexpr uint32_t instruction = f8_instruction(kCtas * kRowTile, 128, kTransposed);
+                // this half's columns in a block's share of the weight: 128 / kCtas of them
+                constexpr int kHalfBytes = kTransposed ? (kCtas == 2 ? 64 : 128 * kBlockK) : 128 / kCtas * kBlockK;
+                // 32 channels on: 32 bytes along a K-major row, 32 rows of 128 bytes MN-major
+                constexpr int kStepW = (kTransposed ? 32 * 128 : 32) >> 4, kStepA = 32 >> 4;
+                const uint64_t a0 = smem_descriptor(tiles_at, 16, 1024);
+                const uint64_t w0 = smem_descriptor(tiles_at + kStageA + half * kHalfBytes, 16, 1024);
+                Ring r;
+                uint32_t parities = 0;   // of the accumulators' passes, a bit per stage of a group
+                for (long long t = blockIdx.x; go && t < total * kCtas; t += gridDim.x) {
+                    for (int kb = 0; kb < nkb; ++kb) {
+                        const int slot = kb % Layout::kGroup, buffer = slot * Layout::kHalves + half;
+                        const bool free_now =
+                            mbar_wait_polls(at(&s.acc_empty[buffer]), ((parities >> slot) & 1u) ^ 1u);
+                        const bool full_now = mbar_wait_polls(at(&s.full[r.slot]), r.parity);
+                        tcgen05_fence_after();
+                        const uint64_t da = a0 + (uint32_t)r.slot * (Layout::kStageBytes >> 4);
+                        const uint64_t dw = w0 + (uint32_t)r.slot * (Layout::kStageBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < kBlockK / 32; ++k) {
-                        // 32 channels on: 32 bytes along a K-major row, 32 rows of 128 bytes MN-major
-                        const uint64_t da = smem_descriptor(a + k * 32, 16, 1024);
-                        const uint64_t dw = kTransposed ? smem_descriptor(w + k * 32 * 128, 128 * kBlockK, 1024)
-                                                        : smem_descriptor(w + k * 32, 16, 1024);
-                        mma_f8<kCtas>(tmem + b.slot * kBN, da, dw, instruction, k > 0);
+                        for (int k = 0; k < kBlockK / 32; ++k)
+                            mma_f8<kCtas>(tmem + buffer * 128, da + k * kStepA, dw + k * kStepW, instruction, k > 0,
+                                          issue);
+                        mma_commit<kCtas>(at(&s.acc_full[buffer]), issue);
+                        mma_commit<kCtas>(at(&s.empty[r.slot]), issue);
+                        parities ^= 1u << slot;
+                        r.advance(Layout::kStages);
+                        go = __all_sync(0xffffffffu, free_now && full_now);
+                        if (!go) break;
                     }
-                    mma_commit<kCtas>(&s.empty[r.slot]);
-                    mma_commit<kCtas>(&s.acc_full[b.slot]);
-                    r.advance(Layout::kStages);
-                    b.advance(Layout::kBuffers);
+                }
+                if (!go) {   // leave no product running
+                    mma_commit<kCtas>(at(&s.drain[half]), issue);
+                    mbar_wait_polls(at(&s.drain[half]), 0);
                 }
             }
-            if (!go) {   // leave no product running
-                mma_commit<kCtas>(&s.drain);
-                mbar_wait_bounded(&s.drain, 0);
+        } else if (warp == 11) {
+            // --------------------------------------------------- scales
+            const int nb = (p.N + 127) / 128;           // scale blocks along the columns
+            const size_t step = kTransposed ? nb : 1;   // from one block of channels to the next
+            Ring c;
+            for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
+                const Tile tile = tile_at<kCtas>(s, p, t, rank);
+                const float *sw[Layout::kHalves];
+#pragma unroll
+                for (int h = 0; h < Layout::kHalves; ++h) {
+                    // the block of a half's columns; a pair's warpgroups use one each (the same block
+                    // for both halves), so there `h` is the warpgroup
+                    const int block = kGated ? h * (nb / 2) + tile.n : min(tile.n * Layout::kHalves + h, nb - 1);
+                    sw[h] = p.w_scale + (size_t)tile.e * nkb * nb + (kTransposed ? (size_t)block : (size_t)block * nkb);
+                }
+                for (int kb0 = 0; kb0 < nkb; kb0 += Layout::kGroup) {
+                    float fa[4][Layout::kGroup], fw[Layout::kHalves][Layout::kGroup];
+#pragma unroll
+                    for (int i = 0; i < Layout::kGroup; ++i) {
+                        const int kb = min(kb0 + i, nkb - 1);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = q * 32 + lane;
+                            fa[q][i] = r < tile.valid ? __ldg(p.a_scale + ((size_t)tile.row0 + r) * nkb + kb) : 0.0f;
+                        }
+#pragma unroll
+                        for (int h = 0; h < Layout::kHalves; ++h) fw[h][i] = __ldg(sw[h] + kb * step);
+                    }
+                    go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.scale_empty[c.slot]), c.parity ^ 1u));
+                    if (!go) break;
+#pragma unroll
+                    for (int i = 0; i < Layout::kGroup; ++i)
+#pragma unroll
+                        for (int h = 0; h < Layout::kHalves; ++h)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                s.scales[c.slot][i * Layout::kHalves + h][q * 32 + lane] = fa[q][i] * fw[h][i];
+                    __syncwarp();
+                    mbar_arrive(at(&s.scale_full[c.slot]), issue);
+                    c.advance(kScaleSlots);
+                }
             }
         }
-        __syncwarp();
     } else {
         // ------------------------------------- scaled sums and the output
         registers_increase<kSumRegisters>();
-        constexpr int kCols = kBN / 2;            // columns of a warpgroup
+        // of a unit's 128 columns a warpgroup takes 64, so kHalves * 64 of the tile's
+        constexpr int kHalves = Layout::kHalves, kGroup = Layout::kGroup;
         const int wg = warp >> 2, quarter = warp & 3;
         unsigned char *stage = tiles + Layout::kStaging + warp * kStagingWarp;
-        const int nb = (p.N + 127) / 128;         // scale blocks along the columns
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        Ring b;
-        uint32_t pair_parity = 0;
-        bool go = true;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + wg * 64;
+        Ring c;
+        uint32_t parities = 0, pair_parity = 0;
         for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
             const Tile tile = tile_at<kCtas>(s, p, t, rank);
             const int nrows = min(tile.valid - quarter * 32, 32);   // rows of this warp
-            const int n0 = kGated ? tile.n * 128 : tile.n * kBN + wg * kCols;
-            const bool active = nrows > 0 && (kGated || n0 < p.N);
-            const size_t row = (size_t)tile.row0 + quarter * 32 + min(lane, max(nrows, 1) - 1);
-            const float *sa = p.a_scale + (active ? row : 0) * nkb;
-            // the weight scales of block b: sw[b * step] (and su for the up projection's block)
-            const size_t step = kTransposed ? nb : 1;
-            const int cblock = active ? n0 / 128 : 0;
-            const float *sw = p.w_scale + (kTransposed ? (size_t)tile.e * nkb * nb + cblock
-                                                       : ((size_t)tile.e * nb + cblock) * nkb);
-            const float *su = kGated ? sw + (size_t)(nb / 2) * nkb : nullptr;
+            // first of the 64 columns of each half: with a pair, a unit's columns are 64 of each
+            // block's 128.  Gated: half 0 is the gate, half 1 the up projection
+            int col[kHalves];
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+                col[h] = kGated ? tile.n * 128 + wg * 64
+                                : tile.n * kBN + (kCtas == 2 ? wg * 128 + h * 64 : h * 128 + wg * 64);
+            const bool active = nrows > 0 && (kGated || col[0] < p.N);
 
-            float2 acc[kCols / 2];
+            float2 acc[kHalves * 32];
 #pragma unroll
-            for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            // scales are fetched a group of four blocks ahead
-            float fa[4], fw[4], fu[4];
+            for (int i = 0; i < kHalves * 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            for (int kb0 = 0; kb0 < nkb; kb0 += kGroup) {
+                bool ok = mbar_wait_polls(at(&s.scale_full[c.slot]), c.parity);
+                const float *f0 = &s.scales[c.slot][0][quarter * 32 + lane];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                fa[i] = i < nkb ? __ldg(sa + i) : 0.0f;
-                fw[i] = i < nkb ? __ldg(sw + i * step) : 0.0f;
-                if (kGated) fu[i] = i < nkb ? __ldg(su + i) : 0.0f;
-            }
-            for (int kb0 = 0; go && kb0 < nkb; kb0 += 4) {
-                float f[4], g[4];
+                for (int i = 0; i < kGroup; ++i) {
+                    if (i > 0 && kb0 + i >= nkb) break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[i] = fa[i] * fw[i];
-                    if (kGated) g[i] = fa[i] * fu[i];
-                    const int kb = kb0 + 4 + i;
-                    if (kb < nkb) {
-                        fa[i] = __ldg(sa + kb);
-                        fw[i] = __ldg(sw + kb * step);
-                        if (kGated) fu[i] = __ldg(su + kb);
-                    }
-                }
+                    for (int h = 0; h < kHalves; ++h) {
+                        const int buffer = i * kHalves + h;
+                        // a pair's columns of one warpgroup are in one scale block
+                        const float f = kCtas == 2 && !kGated ? f0[(i * kHalves + wg) * kRowTile] : f0[buffer * kRowTile];
+                        ok = mbar_wait_polls(at(&s.acc_full[buffer]), (parities >> i) & 1u) && ok;
+                        tcgen05_fence_after();
+                        // every warp adds, rows past its own included: a branch would cost more
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (kb0 + i >= nkb) break;
-                    go = __all_sync(0xffffffffu, wait_or_stop(s, &s.acc_full[b.slot], b.parity));
-                    if (!go) break;
-                    tcgen05_fence_after();
-                    if (active) {
-                        // the next columns are on their way while these are added
-                        uint32_t v[2][kChunk];
-                        const uint32_t at = lanes + b.slot * kBN;
-                        tmem_load(at + chunk_column<kCols, kGated>(wg, 0), v[0]);
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t r[32];
+                            tmem_load(lanes + buffer * 128 + k * 32, r);
+                            tmem_wait_load(r);
+                            if (k == 1) {   // all read: the accumulator is free
+                                tcgen05_fence_before();
+                                if (kCtas == 2) mbar_arrive_first(at(&s.acc_empty[buffer]), issue);
+                                else mbar_arrive(at(&s.acc_empty[buffer]), issue);
+                            }
 #pragma unroll
-                        for (int c = 0; c < kCols / kChunk; ++c) {
-                            tmem_wait_load();
-                            if (c + 1 < kCols / kChunk)
-                                tmem_load(at + chunk_column<kCols, kGated>(wg, (c + 1) * kChunk), v[(c + 1) & 1]);
-                            const float fc = (kGated && c * kChunk >= 64) ? g[i] : f[i];
-#pragma unroll
-                            for (int k = 0; k < kChunk / 2; ++k)
-                                fma_pair(acc[c * (kChunk / 2) + k], make_float2(fc, fc),
-                                         make_float2(__uint_as_float(v[c & 1][2 * k]),
-                                                     __uint_as_float(v[c & 1][2 * k + 1])));
+                            for (int j = 0; j < 16; ++j)
+                                fma_pair(acc[h * 32 + k * 16 + j], make_float2(f, f),
+                                         make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
                         }
                     }
-                    tcgen05_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (kCtas == 2) mbar_arrive_first(&s.acc_empty[b.slot]);
-                        else mbar_arrive(&s.acc_empty[b.slot]);
-                    }
-                    b.advance(Layout::kBuffers);
+                    parities ^= 1u << i;
                 }
+                __syncwarp();
+                mbar_arrive(at(&s.scale_empty[c.slot]), issue);
+                c.advance(kScaleSlots);
+                go = __all_sync(0xffffffffu, ok);
+                if (!go) break;
             }
             if (!go) break;
             const size_t warp_row = (size_t)tile.row0 + quarter * 32;
             if constexpr (kGated) {
-                const int I = p.N / 2, i0 = n0 + wg * 64;
+                const int I = p.N / 2, i0 = col[0];
                 if (p.h && active) {
                     unsigned char *h = reinterpret_cast<unsigned char *>(p.h + warp_row * p.N + i0);
                     store_bf16x64(acc, stage, h, (size_t)p.N * 2, nrows, 128, lane);
@@ -465,8 +484,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 // again only after the other has arrived for the tile in between, so after its read
                 s.amax[pair_parity][wg][quarter * 32 + lane] = amax;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.pair[quarter]);
-                go = __all_sync(0xffffffffu, wait_or_stop(s, &s.pair[quarter], pair_parity));
+                mbar_arrive(at(&s.pair[quarter]), issue);
+                go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.pair[quarter]), pair_parity));
                 if (!go) break;
                 amax = quant_amax(fmaxf(amax, s.amax[pair_parity][wg ^ 1][quarter * 32 + lane]));
                 pair_parity ^= 1u;
@@ -489,34 +508,35 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         p.q_scale[(warp_row + lane) * (I / 128) + tile.n] = quant_scale(amax);
                 }
             } else if (active) {
-                if (p.out_f32) {
 #pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c) {
+                for (int h = 0; h < kHalves; ++h) {
+                    if (col[h] >= p.N) break;
+                    if (!p.out_f32) {
+                        store_bf16x64(acc + h * 32, stage,
+                                      static_cast<unsigned char *>(p.out) + (warp_row * p.N + col[h]) * 2,
+                                      (size_t)p.N * 2, nrows, (p.N - col[h]) * 2, lane);
+                        continue;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
                         uint4 v[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float2 v0 = acc[c * 16 + 2 * k], v1 = acc[c * 16 + 2 * k + 1];
+                            const float2 v0 = acc[h * 32 + c * 16 + 2 * k], v1 = acc[h * 32 + c * 16 + 2 * k + 1];
                             v[k] = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
                                               __float_as_uint(v1.y));
                         }
-                        const int n = n0 + c * 32;
+                        const int n = col[h] + c * 32;
                         if (n < p.N)
                             store_rows<8>(v, stage, static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 4,
                                           (size_t)p.N * 4, nrows, (p.N - n) * 4, lane);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < kCols / 64; ++c) {
-                        const int n = n0 + c * 64;
-                        if (n < p.N)
-                            store_bf16x64(acc + c * 32, stage,
-                                          static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 2,
-                                          (size_t)p.N * 2, nrows, (p.N - n) * 2, lane);
                     }
                 }
             }
         }
     }
+    if (!go && issue) atomicOr(&g_product_error, MOE_DEVERR_COPY_TIMEOUT);
+    __syncwarp();
     tcgen05_fence_before();
     if (kCtas == 2) cluster_barrier();   // nothing of the other block's reaches this one any more
     else __syncthreads();

@@ -39,30 +39,30 @@ __device__ __forceinline__ void tmem_free(uint32_t base) {
     else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(kColumns));
 }
 
-// 32 lanes x 16 columns of fp32: thread = lane (row), one register per column.
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-}
-
 // 32 lanes x 32 columns of fp32: thread = lane (row), one register per column.
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads of tensor memory this thread has issued.  Nothing may
+// touch a load's registers before, so they pass through here.
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :
+        : "memory");
+}
 __device__ __forceinline__ void tcgen05_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -84,43 +84,57 @@ __device__ __forceinline__ uint64_t smem_descriptor(uint32_t addr, uint32_t lead
 }
 
 // Instruction descriptor: e4m3 x e4m3, fp32 accumulators, M x N, A K-major.
-__device__ __forceinline__ uint32_t f8_instruction(int M, int N, bool b_mn_major) {
+__host__ __device__ constexpr uint32_t f8_instruction(int M, int N, bool b_mn_major) {
     return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// One thread (of a pair's first block): d (tensor memory) = a x b, or += with
-// accumulate; K = 32.
+// The instructions below that one thread issues take `issue`: the warp runs
+// them together and the thread that has it set issues.  A predicate costs
+// nothing, where a branch around them splits the warp and joins it again
+// (tens of cycles each time, on the path that feeds the tensor cores).
+
+// d (tensor memory) = a x b, or += with accumulate; K = 32.  One thread of a
+// block, of a pair's first block.
 template <int kCtas>
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t instruction, bool accumulate) {
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t instruction, bool accumulate,
+                                       bool issue) {
     if (kCtas == 2)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(instruction), "r"((uint32_t)accumulate)
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(instruction), "r"((uint32_t)accumulate), "r"((uint32_t)issue)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(instruction), "r"((uint32_t)accumulate)
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(instruction), "r"((uint32_t)accumulate), "r"((uint32_t)issue)
             : "memory");
 }
 
 // Arrives once on `bar` (of both blocks of a pair) when every product this
 // thread has issued is complete.
 template <int kCtas>
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, bool issue) {
     if (kCtas == 2)
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                smem_u32(bar)),
-            "h"((uint16_t)3)
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+                "r"(bar),
+            "h"((uint16_t)3), "r"((uint32_t)issue)
             : "memory");
     else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                     : "memory");
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+            "r"((uint32_t)issue)
+            : "memory");
 }
 
 // ------------------------------------------------------ tiled tensor loads
@@ -128,39 +142,49 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 // Into this block's shared memory; the bytes count on `bar`, for a pair on the
 // barrier at that place in its first block.
 template <int kCtas>
-__device__ __forceinline__ uint32_t barrier_address(uint64_t *bar) {
-    return kCtas == 2 ? smem_u32(bar) & 0xfeffffffu : smem_u32(bar);   // bit 24: which block of the pair
+__device__ __forceinline__ uint32_t barrier_address(uint32_t bar) {
+    return kCtas == 2 ? bar & 0xfeffffffu : bar;   // bit 24: which block of the pair
 }
 
 template <int kCtas>
-__device__ __forceinline__ void tensor_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+__device__ __forceinline__ void tensor_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar,
+                                               bool issue) {
     if (kCtas == 2)
         asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-            "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-            "l"(map), "r"(x), "r"(y), "r"(barrier_address<2>(bar))
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+            "[%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(barrier_address<2>(bar)), "r"((uint32_t)issue)
             : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-            "[%4];" ::"r"(smem_u32(dst)),
-            "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+            "[%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(barrier_address<1>(bar)), "r"((uint32_t)issue)
             : "memory");
 }
 
 template <int kCtas>
-__device__ __forceinline__ void tensor_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+__device__ __forceinline__ void tensor_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar,
+                                               bool issue) {
     if (kCtas == 2)
         asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-            "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-            "l"(map), "r"(x), "r"(y), "r"(z), "r"(barrier_address<2>(bar))
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %6, 0;\n\t"
+            "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+            "[%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(barrier_address<2>(bar)), "r"((uint32_t)issue)
             : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-            "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-            "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %6, 0;\n\t"
+            "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+            "[%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(barrier_address<1>(bar)), "r"((uint32_t)issue)
             : "memory");
 }
 
@@ -170,18 +194,56 @@ __device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap *map) {
 
 // ---------------------------------------------------------------- barriers
 
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// Waits for a barrier's phase with a limit of about a second: false if it did
+// not complete.  The limit counts polls (about 55 cycles each, and a poll that
+// does not suspend the warp), so that a wait costs no look at a clock.
+__device__ __forceinline__ bool mbar_wait_polls(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, more;\n\t.reg .b32 n;\n\t"
+        "mov.b32 n, 33554432;\n"
+        "POLL:\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.s32 n, n, 1;\n\t"
+        "setp.gt.s32 more, n, 0;\n\t"
+        "@more bra POLL;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar, bool issue) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"((uint32_t)issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes, bool issue) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"((uint32_t)issue)
+        : "memory");
 }
 
 // Arrives on the barrier at this place in the first block of the cluster.
 // Relaxed: what it orders are reads of tensor memory, behind tcgen05 fences (a
 // release at cluster scope took about 900 cycles, twice a stage's products).
-__device__ __forceinline__ void mbar_arrive_first(uint64_t *bar) {
+__device__ __forceinline__ void mbar_arrive_first(uint32_t bar, bool issue) {
     asm volatile(
-        "{\n\t.reg .b32 a;\n\t"
+        "{\n\t.reg .b32 a;\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
         "mapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+        "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar),
+        "r"((uint32_t)issue)
         : "memory");
 }
 

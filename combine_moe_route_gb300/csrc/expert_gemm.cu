@@ -72,18 +72,14 @@ struct ProductArgs {
     __nv_bfloat16 *h;   // gated form: [rows, N] or null
 };
 
-// kCtas blocks work on one tile of kCtas * 128 rows x kBN columns.  A stage's
-// product is done 128 columns at a time (kHalves units), each into an
-// accumulator of its own: four accumulators keep the tensor cores busy across
-// the round trip accumulator -> sums -> accumulator free, about 1300 cycles
-// with a unit's product itself, which two of 256 columns did not.
+// kCtas blocks work on one tile of kCtas * 128 rows x kBN columns; every stage's
+// product goes to the next of kGroup accumulators.
 template <int kCtas, int kBN>
 struct ProductLayout {
-    static constexpr int kHalves = kBN / 128;
     static constexpr int kStageBytes = kStageA + kBN / kCtas * kBlockK;
     static constexpr int kStages = 192 * 1024 / kStageBytes;
-    static constexpr int kBuffers = kTmemColumns / 128;
-    static constexpr int kGroup = kBuffers / kHalves;   // stages that fill every accumulator once
+    static constexpr int kGroup = kTmemColumns / kBN;
+    static constexpr int kHalves = kBN / 128;   // 64-column groups of a warpgroup
     static constexpr int kStaging = kStages * kStageBytes;
     static constexpr int kBytes = kStaging + 8 * kStagingWarp + 1024;   // + alignment of the swizzled tiles
 };
@@ -93,7 +89,7 @@ struct ProductLayout {
 // the up projection's columns lie apart.
 template <int kCtas, int kBN, bool kTransposed, bool kGated>
 constexpr int weight_box() {
-    return kGated ? 128 / kCtas : kTransposed ? 128 : kBN / kCtas;
+    return (kTransposed || kGated) ? 128 : kBN / kCtas;
 }
 
 // Bytes that a row tile's load of A brings.
@@ -104,14 +100,14 @@ __device__ __forceinline__ uint32_t row_load_bytes(int valid) {
 template <int kCtas, int kBN>
 struct ProductShared {
     uint64_t full[ProductLayout<kCtas, kBN>::kStages], empty[ProductLayout<kCtas, kBN>::kStages];
-    uint64_t acc_full[ProductLayout<kCtas, kBN>::kBuffers], acc_empty[ProductLayout<kCtas, kBN>::kBuffers];
+    uint64_t acc_full[ProductLayout<kCtas, kBN>::kGroup], acc_empty[ProductLayout<kCtas, kBN>::kGroup];
     uint64_t pair[4];                      // gated: the two warps that share a quarter of the rows
     uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
     uint64_t drain[2];
     uint32_t tmem;
     int32_t warp_tiles[kProductThreads / 32];
     int32_t tiles[MOE_MAX_EXPERTS + 1];    // row tiles before expert e
-    float scales[kScaleSlots][ProductLayout<kCtas, kBN>::kBuffers][kRowTile];   // a_scale * w_scale of a group
+    float scales[kScaleSlots][4][kRowTile];   // a_scale * w_scale: a group's stages, kHalves each
     float amax[2][2][kRowTile];            // gated: by tile parity, each warpgroup's maximum of a row's block
 };
 
@@ -209,9 +205,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < Layout::kStages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], Layout::kHalves);
+            mbar_init(&s.empty[i], 1);
         }
-        for (int i = 0; i < Layout::kBuffers; ++i) {
+        for (int i = 0; i < Layout::kGroup; ++i) {
             mbar_init(&s.acc_full[i], 1);
             mbar_init(&s.acc_empty[i], 8 * kCtas);
         }
@@ -282,7 +278,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 // a pair splits the columns: each block brings half of them
                 constexpr int kBox = weight_box<kCtas, kBN, kTransposed, kGated>(), kBoxBytes = kBox * kBlockK;
                 constexpr int kBoxes = kBN / kCtas / kBox;
-                const int first = n0 + rank * (kGated ? 64 : 128);
+                const int first = n0 + rank * (kGated ? p.N / 2 : 128);
                 const CUtensorMap *rows = tile.valid > kFewRows ? &map_a : &map_few;
                 const uint32_t bytes =
                     kCtas * kBoxes * kBoxBytes +
@@ -317,45 +313,45 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (!go && rank == 0)   // a pair's barrier counts both blocks' loads
                     mbar_wait_polls(at(&s.full[r.slot]), r.parity);
             }
-        } else if (warp < 9 + Layout::kHalves) {
+        } else if (warp < 11) {
             // ------------------------------------------------- products
-            // one warp per half: a thread issues about as fast as its products run, so one alone
-            // would leave the tensor cores idle while it waits on barriers
+            // two warps take turns: a thread issues about as fast as its products run, so one
+            // alone would leave the tensor cores idle while it waits on barriers
             if (rank == 0) {
-                const int half = warp - 9;
-                constexpr uint32_t instruction = f8_instruction(kCtas * kRowTile, 128, kTransposed);
-                // this half's columns in a block's share of the weight: 128 / kCtas of them
-                constexpr int kHalfBytes = kTransposed ? (kCtas == 2 ? 64 : 128 * kBlockK) : 128 / kCtas * kBlockK;
+                const int turn = warp - 9;
+                constexpr uint32_t instruction = f8_instruction(kCtas * kRowTile, kBN, kTransposed);
                 // 32 channels on: 32 bytes along a K-major row, 32 rows of 128 bytes MN-major
                 constexpr int kStepW = (kTransposed ? 32 * 128 : 32) >> 4, kStepA = 32 >> 4;
                 const uint64_t a0 = smem_descriptor(tiles_at, 16, 1024);
-                const uint64_t w0 = smem_descriptor(tiles_at + kStageA + half * kHalfBytes, 16, 1024);
+                const uint64_t w0 = smem_descriptor(tiles_at + kStageA, kTransposed ? 128 * kBlockK : 16, 1024);
                 Ring r;
-                uint32_t parities = 0;   // of the accumulators' passes, a bit per stage of a group
+                uint32_t parities = 0;   // of the accumulators' passes
                 for (long long t = blockIdx.x; go && t < total * kCtas; t += gridDim.x) {
                     for (int kb = 0; kb < nkb; ++kb) {
-                        const int slot = kb % Layout::kGroup, buffer = slot * Layout::kHalves + half;
-                        const bool free_now =
-                            mbar_wait_polls(at(&s.acc_empty[buffer]), ((parities >> slot) & 1u) ^ 1u);
-                        const bool full_now = mbar_wait_polls(at(&s.full[r.slot]), r.parity);
-                        tcgen05_fence_after();
-                        const uint64_t da = a0 + (uint32_t)r.slot * (Layout::kStageBytes >> 4);
-                        const uint64_t dw = w0 + (uint32_t)r.slot * (Layout::kStageBytes >> 4);
+                        if ((kb & 1) == turn) {
+                            const int slot = kb % Layout::kGroup;
+                            const bool free_now =
+                                mbar_wait_polls(at(&s.acc_empty[slot]), ((parities >> slot) & 1u) ^ 1u);
+                            const bool full_now = mbar_wait_polls(at(&s.full[r.slot]), r.parity);
+                            tcgen05_fence_after();
+                            const uint64_t da = a0 + (uint32_t)r.slot * (Layout::kStageBytes >> 4);
+                            const uint64_t dw = w0 + (uint32_t)r.slot * (Layout::kStageBytes >> 4);
 #pragma unroll
-                        for (int k = 0; k < kBlockK / 32; ++k)
-                            mma_f8<kCtas>(tmem + buffer * 128, da + k * kStepA, dw + k * kStepW, instruction, k > 0,
-                                          issue);
-                        mma_commit<kCtas>(at(&s.acc_full[buffer]), issue);
-                        mma_commit<kCtas>(at(&s.empty[r.slot]), issue);
-                        parities ^= 1u << slot;
+                            for (int k = 0; k < kBlockK / 32; ++k)
+                                mma_f8<kCtas>(tmem + slot * kBN, da + k * kStepA, dw + k * kStepW, instruction, k > 0,
+                                              issue);
+                            mma_commit<kCtas>(at(&s.acc_full[slot]), issue);
+                            mma_commit<kCtas>(at(&s.empty[r.slot]), issue);
+                            parities ^= 1u << slot;
+                            go = __all_sync(0xffffffffu, free_now && full_now);
+                            if (!go) break;
+                        }
                         r.advance(Layout::kStages);
-                        go = __all_sync(0xffffffffu, free_now && full_now);
-                        if (!go) break;
                     }
                 }
                 if (!go) {   // leave no product running
-                    mma_commit<kCtas>(at(&s.drain[half]), issue);
-                    mbar_wait_polls(at(&s.drain[half]), 0);
+                    mma_commit<kCtas>(at(&s.drain[turn]), issue);
+                    mbar_wait_polls(at(&s.drain[turn]), 0);
                 }
             }
         } else if (warp == 11) {
@@ -368,8 +364,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const float *sw[Layout::kHalves];
 #pragma unroll
                 for (int h = 0; h < Layout::kHalves; ++h) {
-                    // the block of a half's columns; a pair's warpgroups use one each (the same block
-                    // for both halves), so there `h` is the warpgroup
+                    // h: the gate's and the up projection's block, or the warpgroup's
                     const int block = kGated ? h * (nb / 2) + tile.n : min(tile.n * Layout::kHalves + h, nb - 1);
                     sw[h] = p.w_scale + (size_t)tile.e * nkb * nb + (kTransposed ? (size_t)block : (size_t)block * nkb);
                 }
@@ -404,24 +399,21 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     } else {
         // ------------------------------------- scaled sums and the output
         registers_increase<kSumRegisters>();
-        // of a unit's 128 columns a warpgroup takes 64, so kHalves * 64 of the tile's
+        // a warpgroup takes half of the columns, in groups of 64: of the gate's and of the up
+        // projection's (h = 0, 1), or side by side
         constexpr int kHalves = Layout::kHalves, kGroup = Layout::kGroup;
+        constexpr int kApart = kGated ? 128 : 64;                    // from one group to the next
+        constexpr int kFirst = kGated || kHalves == 1 ? 64 : 128;    // from one warpgroup's first to the other's
         const int wg = warp >> 2, quarter = warp & 3;
         unsigned char *stage = tiles + Layout::kStaging + warp * kStagingWarp;
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + wg * 64;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + wg * kFirst;
         Ring c;
         uint32_t parities = 0, pair_parity = 0;
         for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
             const Tile tile = tile_at<kCtas>(s, p, t, rank);
             const int nrows = min(tile.valid - quarter * 32, 32);   // rows of this warp
-            // first of the 64 columns of each half: with a pair, a unit's columns are 64 of each
-            // block's 128.  Gated: half 0 is the gate, half 1 the up projection
-            int col[kHalves];
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-                col[h] = kGated ? tile.n * 128 + wg * 64
-                                : tile.n * kBN + (kCtas == 2 ? wg * 128 + h * 64 : h * 128 + wg * 64);
-            const bool active = nrows > 0 && (kGated || col[0] < p.N);
+            const int n0 = tile.n * (kGated ? 128 : kBN) + wg * kFirst;   // first column
+            const bool active = nrows > 0 && n0 < p.N;
 
             float2 acc[kHalves * 32];
 #pragma unroll
@@ -432,29 +424,25 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
                     if (i > 0 && kb0 + i >= nkb) break;
+                    ok = mbar_wait_polls(at(&s.acc_full[i]), (parities >> i) & 1u) && ok;
+                    tcgen05_fence_after();
+                    // every warp adds, rows past its own included: a branch would cost more
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h) {
-                        const int buffer = i * kHalves + h;
-                        // a pair's columns of one warpgroup are in one scale block
-                        const float f = kCtas == 2 && !kGated ? f0[(i * kHalves + wg) * kRowTile] : f0[buffer * kRowTile];
-                        ok = mbar_wait_polls(at(&s.acc_full[buffer]), (parities >> i) & 1u) && ok;
-                        tcgen05_fence_after();
-                        // every warp adds, rows past its own included: a branch would cost more
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t r[32];
-                            tmem_load(lanes + buffer * 128 + k * 32, r);
-                            tmem_wait_load(r);
-                            if (k == 1) {   // all read: the accumulator is free
-                                tcgen05_fence_before();
-                                if (kCtas == 2) mbar_arrive_first(at(&s.acc_empty[buffer]), issue);
-                                else mbar_arrive(at(&s.acc_empty[buffer]), issue);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                fma_pair(acc[h * 32 + k * 16 + j], make_float2(f, f),
-                                         make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+                    for (int k = 0; k < kHalves * 4; ++k) {
+                        const int h = k / 4;
+                        const float f = f0[(i * kHalves + (kGated ? h : kHalves == 1 ? 0 : wg)) * kRowTile];
+                        uint32_t r[16];
+                        tmem_load(lanes + i * kBN + h * kApart + (k & 3) * 16, r);
+                        tmem_wait_load(r);
+                        if (k == kHalves * 4 - 1) {   // all read: the accumulator is free
+                            tcgen05_fence_before();
+                            if (kCtas == 2) mbar_arrive_first(at(&s.acc_empty[i]), issue);
+                            else mbar_arrive(at(&s.acc_empty[i]), issue);
                         }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            fma_pair(acc[k * 8 + j], make_float2(f, f),
+                                     make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
                     }
                     parities ^= 1u << i;
                 }
@@ -467,7 +455,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             if (!go) break;
             const size_t warp_row = (size_t)tile.row0 + quarter * 32;
             if constexpr (kGated) {
-                const int I = p.N / 2, i0 = col[0];
+                const int I = p.N / 2, i0 = n0;
                 if (p.h && active) {
                     unsigned char *h = reinterpret_cast<unsigned char *>(p.h + warp_row * p.N + i0);
                     store_bf16x64(acc, stage, h, (size_t)p.N * 2, nrows, 128, lane);
@@ -510,11 +498,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             } else if (active) {
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
-                    if (col[h] >= p.N) break;
+                    const int col = n0 + h * 64;
+                    if (col >= p.N) break;
                     if (!p.out_f32) {
                         store_bf16x64(acc + h * 32, stage,
-                                      static_cast<unsigned char *>(p.out) + (warp_row * p.N + col[h]) * 2,
-                                      (size_t)p.N * 2, nrows, (p.N - col[h]) * 2, lane);
+                                      static_cast<unsigned char *>(p.out) + (warp_row * p.N + col) * 2,
+                                      (size_t)p.N * 2, nrows, (p.N - col) * 2, lane);
                         continue;
                     }
 #pragma unroll
@@ -526,7 +515,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                             v[k] = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
                                               __float_as_uint(v1.y));
                         }
-                        const int n = col[h] + c * 32;
+                        const int n = col + c * 32;
                         if (n < p.N)
                             store_rows<8>(v, stage, static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 4,
                                           (size_t)p.N * 4, nrows, (p.N - n) * 4, lane);

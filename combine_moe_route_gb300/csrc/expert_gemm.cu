@@ -16,8 +16,9 @@
 //   warps 9, 10 issue the products of a stage (4 x K = 32 each, 128 columns)
 //               into the tensor memory's accumulators, four in turn;
 //   warp 11     forms the products of the two scales, one per row, channel block
-//               and half of the columns, some blocks ahead, in a ring of its own
-//               (reading them where they are used stalled the sums on L2);
+//               and 128 columns, some blocks ahead, in a ring of its own (reading
+//               them where they are used stalled the sums on L2), and tells the
+//               sums where their tile is;
 //   warps 0-7   (two warpgroups) read a finished accumulator, one row per
 //               thread and kBN / 2 columns per warpgroup, scale it into
 //               registers, and after the last stage write the tile.
@@ -46,15 +47,15 @@ namespace moe {
 constexpr int kProductThreads = 384;
 // Registers of a thread of the loading and issuing warpgroup and of the two
 // others, out of the 168 that a block of 384 threads starts with:
-// 56 + 2 * 224 = 3 * 168.
-constexpr int kIssueRegisters = 56, kSumRegisters = 224;
+// 40 + 2 * 232 = 3 * 168.
+constexpr int kIssueRegisters = 40, kSumRegisters = 232;
 constexpr int kRowTile = 128;     // rows of a tile: the M of one product
 constexpr int kFewRows = 32;      // rows of the small load of A
 constexpr int kBlockK = 128;      // channels per stage: one scale block, 128 bytes
 constexpr int kStageA = kRowTile * kBlockK;
+constexpr int kStagingWarp = 32 * 64;       // output staging of a warp: 32 rows x 64 bytes
 constexpr int kScaleSlots = 4;             // of the ring of scales
 constexpr int kTmemColumns = 512;
-constexpr int kStagingWarp = 16 * 128;      // output staging of a warp: 16 rows x 128 bytes
 
 // Set when a bounded wait of a product kernel ran out (never in a sound run).
 __device__ int32_t g_product_error;
@@ -108,6 +109,7 @@ struct ProductShared {
     int32_t warp_tiles[kProductThreads / 32];
     int32_t tiles[MOE_MAX_EXPERTS + 1];    // row tiles before expert e
     float scales[kScaleSlots][4][kRowTile];   // a_scale * w_scale: a group's stages, kHalves each
+    int4 tile[kScaleSlots];                // of the group in a slot: first row, rows, first column
     float amax[2][2][kRowTile];            // gated: by tile parity, each warpgroup's maximum of a row's block
 };
 
@@ -148,43 +150,41 @@ __device__ __forceinline__ Tile tile_at(const Shared &s, const ProductArgs &p, l
     return {e, r.x + (m * kCtas + rank) * kRowTile, max(min(valid - rank * kRowTile, kRowTile), 0), i / mt, valid};
 }
 
-// Writes the 16-byte chunks a lane holds of its row (32 rows of a warp, kChunks
-// each) to global memory in whole rows: 16 rows at a time through the warp's
-// staging, swizzled against bank conflicts, then kChunks lanes per row.  `dst`
-// is the address in the warp's row 0, rows lie `pitch` bytes apart; rows at or
-// past nrows and bytes at or past `limit` are not written.
-template <int kChunks>
-__device__ __forceinline__ void store_rows(const uint4 (&v)[kChunks], unsigned char *stage, unsigned char *dst,
-                                           size_t pitch, int nrows, int limit, int lane) {
-    constexpr int kRows = 32 / kChunks;   // rows per store instruction
-    const int c = lane % kChunks;
+// 64 bytes of each of a warp's 32 rows (a lane holds its row's) to global
+// memory, four lanes per row, through the warp's staging, which is swizzled
+// against bank conflicts.  (Each lane writing its own row took three times as
+// long: 32 lines a store.)  `dst` is the address in the warp's row 0, rows lie
+// `pitch` bytes apart; rows at or past nrows and bytes at or past `limit` are
+// not written.
+__device__ __forceinline__ void store_rows64(const uint4 (&v)[4], uint32_t stage, unsigned char *dst, size_t pitch,
+                                             int nrows, int limit, int lane) {
+    __syncwarp();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        __syncwarp();
-        if ((lane >> 4) == half) {
+    for (int c = 0; c < 4; ++c) st_shared_v4(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16), v[c]);
+    __syncwarp();
+    const int c = lane & 3;
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k)
-                *reinterpret_cast<uint4 *>(stage + (lane & 15) * 128 + ((k ^ (lane & 7)) * 16)) = v[k];
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 16 / kRows; ++i) {
-            const int r = i * kRows + lane / kChunks;
-            const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((c ^ (r & 7)) * 16));
-            if (half * 16 + r < nrows && c * 16 < limit) st_v4(dst + (size_t)(half * 16 + r) * pitch + c * 16, x);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        const uint4 x = ld_shared_v4(stage + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
+        if (r < nrows && c * 16 < limit) st_v4(dst + (size_t)r * pitch + c * 16, x);
     }
 }
 
 // 64 fp32 values of a row, as bf16.
-__device__ __forceinline__ void store_bf16x64(const float2 *acc, unsigned char *stage, unsigned char *dst, size_t pitch,
+__device__ __forceinline__ void store_bf16x64(const float2 *acc, uint32_t stage, unsigned char *dst, size_t pitch,
                                               int nrows, int limit, int lane) {
-    uint4 v[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        v[c] = make_uint4(bf16_pair(acc[4 * c].x, acc[4 * c].y), bf16_pair(acc[4 * c + 1].x, acc[4 * c + 1].y),
-                          bf16_pair(acc[4 * c + 2].x, acc[4 * c + 2].y), bf16_pair(acc[4 * c + 3].x, acc[4 * c + 3].y));
-    store_rows<8>(v, stage, dst, pitch, nrows, limit, lane);
+    for (int c = 0; c < 2; ++c) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 *a = acc + c * 16 + i * 4;
+            v[i] = make_uint4(bf16_pair(a[0].x, a[0].y), bf16_pair(a[1].x, a[1].y), bf16_pair(a[2].x, a[2].y),
+                              bf16_pair(a[3].x, a[3].y));
+        }
+        store_rows64(v, stage, dst + c * 64, pitch, nrows, limit - c * 64, lane);
+    }
 }
 
 template <int kCtas, int kBN, bool kTransposed, bool kGated>
@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 s.scales[c.slot][i * Layout::kHalves + h][q * 32 + lane] = fa[q][i] * fw[h][i];
+                    if (issue) s.tile[c.slot] = make_int4(tile.row0, tile.valid, tile.n * (kGated ? 128 : kBN), 0);
                     __syncwarp();
                     mbar_arrive(at(&s.scale_full[c.slot]), issue);
                     c.advance(kScaleSlots);
@@ -405,22 +406,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         constexpr int kApart = kGated ? 128 : 64;                    // from one group to the next
         constexpr int kFirst = kGated || kHalves == 1 ? 64 : 128;    // from one warpgroup's first to the other's
         const int wg = warp >> 2, quarter = warp & 3;
-        unsigned char *stage = tiles + Layout::kStaging + warp * kStagingWarp;
+        const uint32_t stage = tiles_at + Layout::kStaging + warp * kStagingWarp;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + wg * kFirst;
         Ring c;
         uint32_t parities = 0, pair_parity = 0;
         for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
-            const Tile tile = tile_at<kCtas>(s, p, t, rank);
-            const int nrows = min(tile.valid - quarter * 32, 32);   // rows of this warp
-            const int n0 = tile.n * (kGated ? 128 : kBN) + wg * kFirst;   // first column
-            const bool active = nrows > 0 && n0 < p.N;
-
+            int4 tile;
             float2 acc[kHalves * 32];
 #pragma unroll
             for (int i = 0; i < kHalves * 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
             for (int kb0 = 0; kb0 < nkb; kb0 += kGroup) {
                 bool ok = mbar_wait_polls(at(&s.scale_full[c.slot]), c.parity);
                 const float *f0 = &s.scales[c.slot][0][quarter * 32 + lane];
+                if (kb0 == 0) tile = s.tile[c.slot];
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
                     if (i > 0 && kb0 + i >= nkb) break;
@@ -453,11 +451,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (!go) break;
             }
             if (!go) break;
-            const size_t warp_row = (size_t)tile.row0 + quarter * 32;
+            const int nrows = min(tile.y - quarter * 32, 32);   // rows of this warp
+            const int n0 = tile.z + wg * kFirst;                // first column
+            const bool mine = nrows > 0 && n0 < p.N;
+            const size_t warp_row = (size_t)tile.x + quarter * 32;
             if constexpr (kGated) {
-                const int I = p.N / 2, i0 = n0;
-                if (p.h && active) {
-                    unsigned char *h = reinterpret_cast<unsigned char *>(p.h + warp_row * p.N + i0);
+                const int I = p.N / 2;
+                if (p.h && mine) {
+                    unsigned char *h = reinterpret_cast<unsigned char *>(p.h + warp_row * p.N + n0);
                     store_bf16x64(acc, stage, h, (size_t)p.N * 2, nrows, 128, lane);
                     store_bf16x64(acc + 32, stage, h + (size_t)I * 2, (size_t)p.N * 2, nrows, 128, lane);
                 }
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (!go) break;
                 amax = quant_amax(fmaxf(amax, s.amax[pair_parity][wg ^ 1][quarter * 32 + lane]));
                 pair_parity ^= 1u;
-                if (active) {
+                if (mine) {
                     const float inv = quant_inverse(amax);
                     uint4 v[4];
 #pragma unroll
@@ -491,34 +492,32 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         }
                         v[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    store_rows<4>(v, stage, p.q + warp_row * I + i0, I, nrows, 64, lane);
+                    store_rows64(v, stage, p.q + warp_row * I + n0, I, nrows, 64, lane);
                     if (wg == 0 && lane < nrows)
-                        p.q_scale[(warp_row + lane) * (I / 128) + tile.n] = quant_scale(amax);
+                        p.q_scale[(warp_row + lane) * (I / 128) + n0 / 128] = quant_scale(amax);
                 }
-            } else if (active) {
+            } else if (mine) {
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
-                    const int col = n0 + h * 64;
-                    if (col >= p.N) break;
+                    const int n = n0 + h * 64;
                     if (!p.out_f32) {
                         store_bf16x64(acc + h * 32, stage,
-                                      static_cast<unsigned char *>(p.out) + (warp_row * p.N + col) * 2,
-                                      (size_t)p.N * 2, nrows, (p.N - col) * 2, lane);
+                                      static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 2, (size_t)p.N * 2,
+                                      nrows, (p.N - n) * 2, lane);
                         continue;
                     }
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint4 v[8];
+                    for (int c = 0; c < 4; ++c) {
+                        uint4 v[4];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float2 v0 = acc[h * 32 + c * 16 + 2 * k], v1 = acc[h * 32 + c * 16 + 2 * k + 1];
-                            v[k] = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 v0 = acc[h * 32 + c * 8 + 2 * i], v1 = acc[h * 32 + c * 8 + 2 * i + 1];
+                            v[i] = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
                                               __float_as_uint(v1.y));
                         }
-                        const int n = col + c * 32;
-                        if (n < p.N)
-                            store_rows<8>(v, stage, static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 4,
-                                          (size_t)p.N * 4, nrows, (p.N - n) * 4, lane);
+                        store_rows64(v, stage,
+                                     static_cast<unsigned char *>(p.out) + (warp_row * p.N + n + c * 16) * 4,
+                                     (size_t)p.N * 4, nrows, (p.N - n) * 4 - c * 64, lane);
                     }
                 }
             }

@@ -50,8 +50,9 @@ __device__ __forceinline__ float e4m3_to_float(unsigned char b) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
 }
 
-// The logistic function with expf and an IEEE division: for v -> -inf, expf
-// overflows to inf and the result is 0.
-__device__ __forceinline__ float sigmoid(float v) { return __fdiv_rn(1.0f, 1.0f + expf(-v)); }
+// The logistic function with expf and the fast division (2 ulp; an IEEE one
+// made the gates' passes wait on arithmetic): for v -> -inf, expf overflows to
+// inf and the result is 0.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
 
 }  // namespace moe

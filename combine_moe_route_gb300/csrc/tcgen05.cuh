@@ -257,6 +257,17 @@ __device__ __forceinline__ void fence_mbarrier_init() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
+// 16 bytes of shared memory by its address.
+__device__ __forceinline__ void st_shared_v4(uint32_t p, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
+}
+
 // Two fp32 fused multiply-adds: acc = f * v + acc, each rounded as fmaf rounds.
 __device__ __forceinline__ void fma_pair(float2 &acc, float2 f, float2 v) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;"

@@ -25,7 +25,8 @@ __all__ = sorted(_API) + ["workloads", "HostLayerPipeline"]
 
 def __getattr__(name):
     if name in _API:
-        return getattr(import_module(".binding", __name__), name)
+        value = globals()[name] = getattr(import_module(".binding", __name__), name)   # once per name
+        return value
     if name == "workloads":
         return import_module(".workloads", __name__)
     if name == "HostLayerPipeline":

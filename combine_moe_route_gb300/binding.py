@@ -165,7 +165,7 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
     if dtype is not None:
         if (t.dtype not in dtype) if type(dtype) is tuple else (t.dtype is not dtype):
             raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != tuple(shape):
+    if shape is not None and t.shape != (shape if type(shape) is tuple else tuple(shape)):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -723,9 +723,33 @@ def _nblocks(n: int) -> int:
 
 
 def _on(t: torch.Tensor, *others: torch.Tensor | None) -> None:
+    index = t.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
+        if o is not None and o.get_device() != index:
             raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
+
+
+# the current stream's handle without a Stream object (2 us of a small call's 14)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _enqueue(name: str, t: torch.Tensor, stream, *args) -> None:
+    """Call ``name`` of the library with ``args`` and the stream, on t's device."""
+    fn = getattr(_lib or load_library(), name)
+    index = t.get_device()
+    if stream is not None:
+        handle = int(stream.cuda_stream)
+    elif _raw_stream is not None:
+        handle = _raw_stream(index)
+    else:
+        handle = int(torch.cuda.current_stream(index).cuda_stream)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != MOE_OK:
+        raise MoeError(status, name)
 
 
 def _expert_operands(a, a_scale, w, w_scale, expert_offsets, transpose):
@@ -763,11 +787,9 @@ def expert_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
         out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
     _dev(out, "out", out_dtype, (rows, N))
     _on(a, out)
-    with torch.cuda.device(a.device):
-        _check(load_library().moe_expert_gemm(
-            _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(expert_offsets), E, N, C, rows, int(bool(transpose)),
-            _DTYPE_FP32 if out_dtype == torch.float32 else _DTYPE_BF16, _ptr(out), _stream_handle(stream, a.device)),
-            "moe_expert_gemm")
+    _enqueue("moe_expert_gemm", a, stream, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+             expert_offsets.data_ptr(), E, N, C, rows, 1 if transpose else 0,
+             _DTYPE_FP32 if out_dtype is torch.float32 else _DTYPE_BF16, out.data_ptr())
     return out
 
 
@@ -800,10 +822,8 @@ def expert_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w
     if h is not None:
         _dev(h, "h", torch.bfloat16, (rows, N))
     _on(a, out, out_scale, h)
-    with torch.cuda.device(dev):
-        _check(load_library().moe_expert_gated_gemm(
-            _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(expert_offsets), E, inner, C, rows, _ptr(out),
-            _ptr(out_scale), _ptr(h), _stream_handle(stream, dev)), "moe_expert_gated_gemm")
+    _enqueue("moe_expert_gated_gemm", a, stream, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+             expert_offsets.data_ptr(), E, inner, C, rows, out.data_ptr(), out_scale.data_ptr(), _ptr(h))
     return GatedResult(out, out_scale, h)
 
 
@@ -841,10 +861,8 @@ def expert_gated_backward(h: torch.Tensor, dv: torch.Tensor, *, fp8: bool = True
     else:
         out_scale = None
     _on(h, dv, out, out_scale)
-    with torch.cuda.device(dev):
-        _check(load_library().moe_expert_gated_backward(
-            _ptr(h), _ptr(dv), rows, inner, _DTYPE_FP8 if fp8 else _DTYPE_BF16, _ptr(out), _ptr(out_scale),
-            _stream_handle(stream, dev)), "moe_expert_gated_backward")
+    _enqueue("moe_expert_gated_backward", h, stream, h.data_ptr(), dv.data_ptr(), rows, inner,
+             _DTYPE_FP8 if fp8 else _DTYPE_BF16, out.data_ptr(), _ptr(out_scale))
     return out, out_scale
 
 
@@ -901,11 +919,9 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, tok2row: torch.Tensor 
     elif dlogits is not None:
         raise ValueError("the gradient of the logits needs both topk_idx and E")
     _on(y, dout, tok2row, topk_w, topk_idx, out, out_scale, dtopk_w, dlogits)
-    with torch.cuda.device(dev):
-        _check(load_library().moe_combine_backward(
-            _ptr(dout), _ptr(y), _ptr(tok2row), _ptr(topk_w), _ptr(topk_idx), T, K, H, rows, E or 0,
-            _DTYPE_FP8 if fp8 else _DTYPE_BF16, _ptr(out), _ptr(out_scale), _ptr(dtopk_w), _ptr(dlogits),
-            _stream_handle(stream, dev)), "moe_combine_backward")
+    _enqueue("moe_combine_backward", y, stream, dout.data_ptr(), y.data_ptr(), _ptr(tok2row), topk_w.data_ptr(),
+             _ptr(topk_idx), T, K, H, rows, E or 0, _DTYPE_FP8 if fp8 else _DTYPE_BF16, out.data_ptr(),
+             _ptr(out_scale), dtopk_w.data_ptr(), _ptr(dlogits))
     return CombineGrad(out, out_scale, dtopk_w, dlogits)
 
 
@@ -929,8 +945,6 @@ def dispatch_backward(drows: torch.Tensor, tok2row: torch.Tensor, K: int, *,
         out = torch.empty((T, H), dtype=out_dtype, device=drows.device)
     _dev(out, "out", out_dtype, (T, H))
     _on(drows, tok2row, out)
-    with torch.cuda.device(drows.device):
-        _check(load_library().moe_dispatch_backward(
-            _ptr(drows), _ptr(tok2row), T, K, H, rows, _DTYPE_FP32 if out_dtype == torch.float32 else _DTYPE_BF16,
-            _ptr(out), _stream_handle(stream, drows.device)), "moe_dispatch_backward")
+    _enqueue("moe_dispatch_backward", drows, stream, drows.data_ptr(), tok2row.data_ptr(), T, K, H, rows,
+             _DTYPE_FP32 if out_dtype is torch.float32 else _DTYPE_BF16, out.data_ptr())
     return out

@@ -224,6 +224,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         prefetch_tensor_map(&map_w);
     }
     if (warp == 9) tmem_alloc<kCtas, kTmemColumns>(&s.tmem);
+    // up to here nothing is read: this block may have started while the kernel before ran out,
+    // and lets the kernel after do the same
+    pdl_launch_dependents();
+    pdl_wait();
     {
         constexpr int kPer = (MOE_MAX_EXPERTS + kProductThreads - 1) / kProductThreads;
         int mine = 0, mt[kPer];
@@ -595,12 +599,14 @@ static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cud
     cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCtas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, map_a, map_few, map_w, p);
 }
 

@@ -50,9 +50,26 @@ __device__ __forceinline__ float e4m3_to_float(unsigned char b) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
 }
 
-// The logistic function with expf and the fast division (2 ulp; an IEEE one
-// made the gates' passes wait on arithmetic): for v -> -inf, expf overflows to
-// inf and the result is 0.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+// The logistic function with __expf and the fast division: within
+// (1 - s) * (2 + 1.2 |v|) + 2 ulp, so a few ulp wherever s is not tiny (expf and
+// an IEEE division made the gates' passes wait on arithmetic).  For v -> -inf,
+// __expf overflows to inf and the result is 0.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+// Pairs of fp32 in one instruction each, rounded as the single operations are.
+__device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<const unsigned long long &>(a)), "l"(reinterpret_cast<const unsigned long long &>(b)));
+    return r;
+}
+// acc = f * v + acc
+__device__ __forceinline__ void fma_pair(float2 &acc, float2 f, float2 v) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<unsigned long long &>(acc))
+        : "l"(reinterpret_cast<const unsigned long long &>(f)), "l"(reinterpret_cast<const unsigned long long &>(v)));
+}
+__device__ __forceinline__ float2 bf16_pair_floats(uint32_t w) { return make_float2(bf16_pair_lo(w), bf16_pair_hi(w)); }
 
 }  // namespace moe

@@ -268,13 +268,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t p) {
     return v;
 }
 
-// Two fp32 fused multiply-adds: acc = f * v + acc, each rounded as fmaf rounds.
-__device__ __forceinline__ void fma_pair(float2 &acc, float2 f, float2 v) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;"
-        : "+l"(reinterpret_cast<unsigned long long &>(acc))
-        : "l"(reinterpret_cast<const unsigned long long &>(f)), "l"(reinterpret_cast<const unsigned long long &>(v)));
-}
-
 // A warpgroup's share of the block's registers (whole warpgroup; the shares
 // may not sum to more than the block was launched with).
 template <int kRegisters>

@@ -66,6 +66,7 @@ struct ProductArgs {
     int E, N, C;
     int rows;
     int ntiles;         // column tiles
+    bool tails;         // single blocks: only what the pairs' launch before leaves (see below)
     bool out_f32;
     void *out;          // plain form: [rows, N]
     unsigned char *q;   // gated form: [rows, N / 2]
@@ -137,6 +138,18 @@ __device__ __forceinline__ int2 expert_rows(const ProductArgs &p, int e) {
     return make_int2(lo, max(hi - lo, 0));
 }
 
+// Row tiles of an expert with n rows.  Pairs take its whole 256 rows and a rest
+// of more than 128; a rest of up to 128 rows, half of a pair's tile, is a tile
+// of the single blocks' launch that follows (`tails`).  Without pairs single
+// blocks take every 128 rows.
+template <int kCtas>
+__device__ __forceinline__ int row_tiles(const ProductArgs &p, int n) {
+    constexpr int kPair = 2 * kRowTile;
+    if (kCtas == 2) return n / kPair + (n % kPair > kRowTile);
+    if (p.tails) return n % kPair > 0 && n % kPair <= kRowTile;
+    return (n + kRowTile - 1) / kRowTile;
+}
+
 // Tile t: experts in order; within an expert the row tiles of one column tile
 // come first, so that blocks working at the same time share the weight.
 template <int kCtas, class Shared>
@@ -144,10 +157,10 @@ __device__ __forceinline__ Tile tile_at(const Shared &s, const ProductArgs &p, l
     const int e = upper_bound_minus_one(s.tiles, p.E, (int)(t / p.ntiles));
     const int mt = s.tiles[e + 1] - s.tiles[e];
     const int i = (int)(t - (long long)s.tiles[e] * p.ntiles);
-    const int m = i % mt;
     const int2 r = expert_rows(p, e);
-    const int valid = min(r.y - m * (kCtas * kRowTile), kCtas * kRowTile);
-    return {e, r.x + (m * kCtas + rank) * kRowTile, max(min(valid - rank * kRowTile, kRowTile), 0), i / mt, valid};
+    const int m = kCtas == 1 && p.tails ? r.y / (2 * kRowTile) * 2 : i % mt * kCtas;   // in units of 128 rows
+    const int valid = min(r.y - m * kRowTile, kCtas * kRowTile);
+    return {e, r.x + (m + rank) * kRowTile, max(min(valid - rank * kRowTile, kRowTile), 0), i / mt, valid};
 }
 
 // 64 bytes of each of a warp's 32 rows (a lane holds its row's) to global
@@ -225,9 +238,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     if (warp == 9) tmem_alloc<kCtas, kTmemColumns>(&s.tmem);
     // up to here nothing is read: this block may have started while the kernel before ran out,
-    // and lets the kernel after do the same
-    pdl_launch_dependents();
-    pdl_wait();
+    // and lets the kernel after do the same.  The tails' launch reads nothing that the pairs'
+    // writes, so it fills the SMs as those run out: pairs let it start once what came before
+    // them is done, and it waits for them at its own end, for whoever waits for it.
+    if (kCtas == 2) {
+        pdl_wait();
+        pdl_launch_dependents();
+    } else {
+        pdl_launch_dependents();
+        if (!p.tails) pdl_wait();
+    }
     {
         constexpr int kPer = (MOE_MAX_EXPERTS + kProductThreads - 1) / kProductThreads;
         int mine = 0, mt[kPer];
@@ -235,7 +255,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         for (int i = 0; i < kPer; ++i) {
             const int e = threadIdx.x * kPer + i;
             mt[i] = 0;
-            if (e < p.E) mt[i] = (expert_rows(p, e).y + kCtas * kRowTile - 1) / (kCtas * kRowTile);
+            if (e < p.E) mt[i] = row_tiles<kCtas>(p, expert_rows(p, e).y);
             mine += mt[i];
         }
         int sum = mine;
@@ -534,6 +554,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     else __syncthreads();
     tcgen05_fence_after();
     if (warp == 9) tmem_free<kCtas, kTmemColumns>(tmem);
+    if (kCtas == 1 && p.tails) pdl_wait();
 }
 
 // ------------------------------------------------------------------- host
@@ -592,7 +613,8 @@ static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cud
     const int cols = kGated ? kBN / 2 : kBN;
     p.ntiles = ((kGated ? p.N / 2 : p.N) + cols - 1) / cols;
     // no more tiles than this exist; the blocks walk them
-    const long long most = ((long long)p.rows / (kCtas * kRowTile) + (p.rows < p.E ? p.rows : p.E)) * p.ntiles;
+    const long long most = ((p.tails ? 0 : (long long)p.rows / (kCtas * kRowTile)) + (p.rows < p.E ? p.rows : p.E)) *
+                           p.ntiles;
     const int groups = device_sm_count() / kCtas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(kCtas * (most < groups ? (most > 0 ? most : 1) : groups)));
@@ -611,11 +633,21 @@ static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cud
 }
 
 template <bool kTransposed, bool kGated>
-static cudaError_t launch_product(const void *a, const void *w, const ProductArgs &p, cudaStream_t stream) {
-    const bool pairs = p.rows >= (long long)p.E * 192;
-    if (pairs) return launch_tiles<2, 256, kTransposed, kGated>(a, w, p, stream);
-    if constexpr (kGated) return launch_tiles<1, 256, kTransposed, kGated>(a, w, p, stream);
-    else return launch_tiles<1, 128, kTransposed, kGated>(a, w, p, stream);
+static cudaError_t launch_product(const void *a, const void *w, ProductArgs p, cudaStream_t stream) {
+    // pairs where an expert has more than a single block's rows on average
+    if (p.rows > (long long)p.E * kRowTile) {
+        const cudaError_t e = launch_tiles<2, 256, kTransposed, kGated>(a, w, p, stream);
+        if (e != cudaSuccess) return e;
+        p.tails = true;
+        return launch_tiles<1, 256, kTransposed, kGated>(a, w, p, stream);
+    }
+    if constexpr (!kGated) {
+        // tiles of 256 columns read A half as often; where they are few, 128 columns spread over
+        // more SMs
+        const long long tiles = ((long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E)) * ((p.N + 255) / 256);
+        if (tiles < 4 * device_sm_count()) return launch_tiles<1, 128, kTransposed, kGated>(a, w, p, stream);
+    }
+    return launch_tiles<1, 256, kTransposed, kGated>(a, w, p, stream);
 }
 
 cudaError_t launch_expert_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,

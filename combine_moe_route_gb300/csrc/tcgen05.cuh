@@ -189,16 +189,17 @@ __device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap *map) {
 
 // ---------------------------------------------------------------- barriers
 
-// Waits for a barrier's phase with a limit of about a second: false if it did
-// not complete.  The limit counts polls (about 55 cycles each, and a poll that
-// does not suspend the warp), so that a wait costs no look at a clock.
+// Waits for a barrier's phase with a limit of a second or two: false if it did
+// not complete.  The limit counts polls, so that a wait costs no look at a
+// clock: a poll answers in about 55 cycles if the phase is complete and else
+// suspends the warp for up to 1.3 us (measured), until it is.
 __device__ __forceinline__ bool mbar_wait_polls(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p, more;\n\t.reg .b32 n;\n\t"
-        "mov.b32 n, 33554432;\n"
+        "mov.b32 n, 1048576;\n"
         "POLL:\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "@p bra DONE;\n\t"
         "sub.s32 n, n, 1;\n\t"
         "setp.gt.s32 more, n, 0;\n\t"

@@ -6,7 +6,8 @@ layer over it that takes torch tensors.  Importing the package does not load
 the library; the first use of an operation does, and raises ``ImportError``
 if the library has not been built -- there is no fallback.
 
-``workloads`` draws the seeded synthetic inputs.
+``workloads`` draws the seeded synthetic inputs; ``experts`` runs a layer
+with quantised gated experts, forward and backward.
 """
 from importlib import import_module
 
@@ -20,12 +21,17 @@ _API = {
     "GatedResult", "CombineGrad", "get_expert_error",
 }
 
-__all__ = sorted(_API) + ["workloads", "HostLayerPipeline"]
+_LAYER = {"expert_layer", "expert_layer_backward", "ExpertWeights", "ExpertForward", "quantize_blocks"}
+
+__all__ = sorted(_API) + sorted(_LAYER) + ["workloads", "HostLayerPipeline"]
 
 
 def __getattr__(name):
     if name in _API:
         value = globals()[name] = getattr(import_module(".binding", __name__), name)   # once per name
+        return value
+    if name in _LAYER:
+        value = globals()[name] = getattr(import_module(".experts", __name__), name)
         return value
     if name == "workloads":
         return import_module(".workloads", __name__)

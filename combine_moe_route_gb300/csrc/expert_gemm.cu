@@ -314,14 +314,20 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     if (!go) break;
                     const uint32_t a = tiles_at + r.slot * Layout::kStageBytes, w = a + kStageA;
                     const uint32_t bar = at(&s.full[r.slot]);
-                    mbar_expect(bar, bytes, issue && rank == 0);
-                    tensor_load_2d<kCtas>(a, rows, kb * kBlockK, tile.row0, bar, issue && tile.valid > 0);
+#ifdef MOE_TEST_WITHHOLD_PRODUCT_STAGE
+                    // Test builds only: the loads of this stage never happen, so the waits run out.
+                    const bool load = issue && issued != MOE_TEST_WITHHOLD_PRODUCT_STAGE;
+#else
+                    const bool load = issue;
+#endif
+                    mbar_expect(bar, bytes, load && rank == 0);
+                    tensor_load_2d<kCtas>(a, rows, kb * kBlockK, tile.row0, bar, load && tile.valid > 0);
 #pragma unroll
                     for (int i = 0; i < kBoxes; ++i) {
                         const int n = first + i * (kGated ? p.N / 2 : kBox);
                         if (kTransposed)
-                            tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, n, kb * kBlockK, tile.e, bar, issue);
-                        else tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, kb * kBlockK, n, tile.e, bar, issue);
+                            tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, n, kb * kBlockK, tile.e, bar, load);
+                        else tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, kb * kBlockK, n, tile.e, bar, load);
                     }
                     r.advance(Layout::kStages);
                     ++issued;

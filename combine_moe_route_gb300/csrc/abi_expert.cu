@@ -90,8 +90,8 @@ moe_status moe_dispatch_backward(const void *drows, const int32_t *tok2row, int 
     if (T == 0) return MOE_OK;
     if (!tok2row || !dx || (rows > 0 && !drows)) return MOE_ERR_INVALID_ARG;
     if (!aligned16(drows) || !aligned16(dx)) return MOE_ERR_UNSUPPORTED;
-    return cuda_status(moe::launch_combine(drows, tok2row, nullptr, T, K, H, out_dtype == MOE_DTYPE_FP32, dx, rows,
-                                           (cudaStream_t)stream));
+    return cuda_status(moe::launch_dispatch_backward(drows, tok2row, T, K, H, rows, out_dtype == MOE_DTYPE_FP32, dx,
+                                                     (cudaStream_t)stream));
 }
 
 }  // extern "C"

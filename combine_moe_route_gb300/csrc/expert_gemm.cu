@@ -133,8 +133,8 @@ struct Tile {
 
 // Expert e's first row and number of rows, inside [0, rows] whatever the offsets hold.
 __device__ __forceinline__ int2 expert_rows(const ProductArgs &p, int e) {
-    const int lo = min(max(__ldg(p.expert_offsets + e), 0), p.rows);
-    const int hi = min(max(__ldg(p.expert_offsets + e + 1), 0), p.rows);
+    const int lo = min(max(ld_chained(p.expert_offsets + e), 0), p.rows);
+    const int hi = min(max(ld_chained(p.expert_offsets + e + 1), 0), p.rows);
     return make_int2(lo, max(hi - lo, 0));
 }
 
@@ -406,10 +406,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int r = q * 32 + lane;
-                            fa[q][i] = r < tile.valid ? __ldg(p.a_scale + ((size_t)tile.row0 + r) * nkb + kb) : 0.0f;
+                            fa[q][i] = r < tile.valid ? ld_chained(p.a_scale + ((size_t)tile.row0 + r) * nkb + kb) : 0.0f;
                         }
 #pragma unroll
-                        for (int h = 0; h < Layout::kHalves; ++h) fw[h][i] = __ldg(sw[h] + kb * step);
+                        for (int h = 0; h < Layout::kHalves; ++h) fw[h][i] = ld_chained(sw[h] + kb * step);
                     }
                     go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.scale_empty[c.slot]), c.parity ^ 1u));
                     if (!go) break;

@@ -16,6 +16,24 @@
 
 namespace moe {
 
+// Both kernels here start while the kernel before them in the stream runs out,
+// wait for it before they read, and let the kernel after do the same.
+template <class... Params, class... Args>
+static cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads, size_t smem,
+                                  cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // --------------------------------------------------------------------------
 // combine backward
 // --------------------------------------------------------------------------
@@ -42,9 +60,9 @@ constexpr int kGradBatch = 8;       // copies whose rows are in flight at once
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kGradThreads, kGradBlocks) combine_backward_kernel(
-    const __nv_bfloat16 *__restrict__ dout, const __nv_bfloat16 *__restrict__ y, const int32_t *__restrict__ tok2row,
-    const float *__restrict__ topk_w, const int32_t *__restrict__ topk_idx, int T, int K, int H, long long rows, int E,
-    void *__restrict__ dy, float *__restrict__ dy_scale, float *__restrict__ dtopk_w, float *__restrict__ dlogits) {
+    const __nv_bfloat16 *dout, const __nv_bfloat16 *y, const int32_t *tok2row,
+    const float *topk_w, const int32_t *topk_idx, int T, int K, int H, long long rows, int E,
+    void *dy, float *dy_scale, float *dtopk_w, float *dlogits) {
     extern __shared__ float s_dl[];   // [E] when dlogits is wanted
     __shared__ int32_t s_row[MOE_MAX_TOPK];
     __shared__ float s_w[MOE_MAX_TOPK];
@@ -54,11 +72,13 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks) combine_backward_ke
     const int nchunk = H / 8;
     const int nchunk_warp = (nchunk + 31) & ~31;   // whole warps, so that the shuffles are uniform
     const long long g = blockIdx.x;
+    pdl_launch_dependents();
+    pdl_wait();
 
     if (threadIdx.x < K) {
-        const long long r = tok2row ? (long long)__ldg(tok2row + g * K + threadIdx.x) : g * K + threadIdx.x;
+        const long long r = tok2row ? (long long)ld_chained(tok2row + g * K + threadIdx.x) : g * K + threadIdx.x;
         s_row[threadIdx.x] = (r >= 0 && r < rows) ? (int32_t)r : -1;
-        s_w[threadIdx.x] = __ldg(topk_w + g * K + threadIdx.x);
+        s_w[threadIdx.x] = ld_chained(topk_w + g * K + threadIdx.x);
     }
     if (dlogits)
         for (int e = threadIdx.x; e < E; e += blockDim.x) s_dl[e] = 0.0f;
@@ -74,9 +94,9 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks) combine_backward_ke
 #pragma unroll
             for (int jj = 0; jj < kGradBatch; ++jj) {
                 const int r = (j0 + jj < K) ? s_row[j0 + jj] : -1;
-                v[jj] = (in && r >= 0) ? ld_stream_v4(y + (size_t)r * H + (size_t)c * 8) : make_uint4(0u, 0u, 0u, 0u);
+                v[jj] = (in && r >= 0) ? ld_chained_v4(y + (size_t)r * H + (size_t)c * 8) : make_uint4(0u, 0u, 0u, 0u);
             }
-            const uint4 dv = in ? *reinterpret_cast<const uint4 *>(dout + (size_t)g * H + (size_t)c * 8)
+            const uint4 dv = in ? ld_chained_v4(dout + (size_t)g * H + (size_t)c * 8)
                                 : make_uint4(0u, 0u, 0u, 0u);
             const float2 d[4] = {bf16_pair_floats(dv.x), bf16_pair_floats(dv.y), bf16_pair_floats(dv.z),
                                  bf16_pair_floats(dv.w)};
@@ -139,7 +159,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks) combine_backward_ke
     if (threadIdx.x < K) {
         float mean = 0.0f;
         for (int i = 0; i < K; ++i) mean = __fmaf_rn(s_w[i], s_dw[i], mean);
-        const int e = __ldg(topk_idx + g * K + threadIdx.x);
+        const int e = ld_chained(topk_idx + g * K + threadIdx.x);
         if (e >= 0 && e < E) s_dl[e] = s_w[threadIdx.x] * (s_dw[threadIdx.x] - mean);
     }
     __syncthreads();
@@ -154,13 +174,9 @@ cudaError_t launch_combine_backward(const void *dout, const void *y, const int32
     const int nchunk = H / 8, rounds = (nchunk + kGradThreads - 1) / kGradThreads;
     const int threads = ((nchunk + rounds - 1) / rounds + 31) / 32 * 32;
     const __nv_bfloat16 *db = static_cast<const __nv_bfloat16 *>(dout), *yb = static_cast<const __nv_bfloat16 *>(y);
-    if (fp8)
-        combine_backward_kernel<true><<<(unsigned)T, threads, smem, stream>>>(
-            db, yb, tok2row, topk_w, topk_idx, T, K, H, rows, E, dy, dy_scale, dtopk_w, dlogits);
-    else
-        combine_backward_kernel<false><<<(unsigned)T, threads, smem, stream>>>(
-            db, yb, tok2row, topk_w, topk_idx, T, K, H, rows, E, dy, dy_scale, dtopk_w, dlogits);
-    return cudaGetLastError();
+    return launch_chained(fp8 ? combine_backward_kernel<true> : combine_backward_kernel<false>, (unsigned)T, threads,
+                          smem, stream, db, yb, tok2row, topk_w, topk_idx, T, K, H, rows, E, dy, dy_scale, dtopk_w,
+                          dlogits);
 }
 
 // --------------------------------------------------------------------------
@@ -181,10 +197,12 @@ constexpr int kGateThreads = 128;
 constexpr int kGateChunks = 2;   // per thread, all loaded before the first is used
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kGateThreads) gated_backward_kernel(const __nv_bfloat16 *__restrict__ h,
-                                                                      const __nv_bfloat16 *__restrict__ da,
-                                                                      long long rows, int I, void *__restrict__ dh,
-                                                                      float *__restrict__ dh_scale) {
+__global__ void __launch_bounds__(kGateThreads) gated_backward_kernel(const __nv_bfloat16 *h,
+                                                                      const __nv_bfloat16 *da,
+                                                                      long long rows, int I, void *dh,
+                                                                      float *dh_scale) {
+    pdl_launch_dependents();
+    pdl_wait();
     const uint32_t nchunk = I / 8;
     const int lane = threadIdx.x & 31;
     // this block's first chunk of 8 channels, by one 64-bit division of the block
@@ -202,9 +220,9 @@ __global__ void __launch_bounds__(kGateThreads) gated_backward_kernel(const __nv
         in[i] = row < rows;
         at[i] = (size_t)row * 2 * I + (size_t)chunk[i] * 8;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        vg[i] = in[i] ? ld_stream_v4(h + at[i]) : zero;
-        vu[i] = in[i] ? ld_stream_v4(h + at[i] + I) : zero;
-        vd[i] = in[i] ? ld_stream_v4(da + (size_t)row * I + (size_t)chunk[i] * 8) : zero;
+        vg[i] = in[i] ? ld_chained_v4(h + at[i]) : zero;
+        vu[i] = in[i] ? ld_chained_v4(h + at[i] + I) : zero;
+        vd[i] = in[i] ? ld_chained_v4(da + (size_t)row * I + (size_t)chunk[i] * 8) : zero;
     }
 #pragma unroll
     for (int i = 0; i < kGateChunks; ++i) {
@@ -262,11 +280,8 @@ cudaError_t launch_gated_backward(const void *h, const void *da, long long rows,
                                   float *dh_scale, cudaStream_t stream) {
     const long long per = kGateThreads * kGateChunks, grid = (rows * (I / 8) + per - 1) / per;
     const __nv_bfloat16 *hb = static_cast<const __nv_bfloat16 *>(h), *db = static_cast<const __nv_bfloat16 *>(da);
-    if (fp8)
-        gated_backward_kernel<true><<<(unsigned)grid, kGateThreads, 0, stream>>>(hb, db, rows, I, dh, dh_scale);
-    else
-        gated_backward_kernel<false><<<(unsigned)grid, kGateThreads, 0, stream>>>(hb, db, rows, I, dh, dh_scale);
-    return cudaGetLastError();
+    return launch_chained(fp8 ? gated_backward_kernel<true> : gated_backward_kernel<false>, (unsigned)grid,
+                          kGateThreads, 0, stream, hb, db, rows, I, dh, dh_scale);
 }
 
 }  // namespace moe

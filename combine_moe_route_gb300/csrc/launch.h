@@ -56,7 +56,6 @@ cudaError_t launch_dispatch_ll(const void *x, const int32_t *topk_idx, const Ran
 cudaError_t launch_dispatch_ll_unordered(const void *x, const int32_t *topk_idx, const RankTable &rt, int E, int K,
                                          int H, int C, bool fp8, void *recv_x, float *recv_scale, int32_t *counts,
                                          int32_t *tok2row, int32_t *row2src, void *workspace, cudaStream_t stream);
-// topk_w == nullptr: unit weights (the gradient of the dispatch scatter).
 cudaError_t launch_combine(const void *y, const int32_t *tok2row, const float *topk_w, int T, int K, int H,
                            bool out_f32, void *out, long long rows, cudaStream_t stream);
 cudaError_t launch_combine_push(const void *y, const int32_t *row2src, const int32_t *counts, int C, int H,
@@ -68,6 +67,8 @@ cudaError_t launch_combine_partial_recv(const void *partial, const int32_t *topk
                                         int R, bool out_f32, void *out, cudaStream_t stream);
 cudaError_t launch_expert_scale(const void *recv, const float *recv_scale, bool fp8, const int32_t *expert_offsets,
                                 int E, int H, int rows, int identity, void *y, cudaStream_t stream);
+cudaError_t launch_dispatch_backward(const void *drows, const int32_t *tok2row, int T, int K, int H, long long rows,
+                                     bool out_f32, void *dx, cudaStream_t stream);
 cudaError_t launch_expert_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,
                                const int32_t *expert_offsets, int E, int N, int C, long long rows, bool transpose,
                                bool out_f32, void *out, cudaStream_t stream);

@@ -452,13 +452,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
                     if (i > 0 && kb0 + i >= nkb) break;
+                    float f[kHalves];   // read here: a read after the wait would wait in its turn
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        f[h] = f0[(i * kHalves + (kGated ? h : kHalves == 1 ? 0 : wg)) * kRowTile];
                     ok = mbar_wait_polls(at(&s.acc_full[i]), (parities >> i) & 1u) && ok;
                     tcgen05_fence_after();
                     // every warp adds, rows past its own included: a branch would cost more
 #pragma unroll
                     for (int k = 0; k < kHalves * 4; ++k) {
                         const int h = k / 4;
-                        const float f = f0[(i * kHalves + (kGated ? h : kHalves == 1 ? 0 : wg)) * kRowTile];
                         uint32_t r[16];
                         tmem_load(lanes + i * kBN + h * kApart + (k & 3) * 16, r);
                         tmem_wait_load(r);
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         }
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            fma_pair(acc[k * 8 + j], make_float2(f, f),
+                            fma_pair(acc[k * 8 + j], make_float2(f[h], f[h]),
                                      make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
                     }
                     parities ^= 1u << i;

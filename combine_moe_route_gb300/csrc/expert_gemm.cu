@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const int wg = warp >> 2, quarter = warp & 3;
         const uint32_t stage = tiles_at + Layout::kStaging + warp * kStagingWarp;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + wg * kFirst;
+        const uint32_t first_empty = kCtas == 2 ? first_block_address(at(&s.acc_empty[0])) : 0;   // 8 bytes each
         Ring c;
         uint32_t parities = 0, pair_parity = 0;
         for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
@@ -445,8 +446,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             float2 acc[kHalves * 32];
 #pragma unroll
             for (int i = 0; i < kHalves * 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            bool ok = true;
             for (int kb0 = 0; kb0 < nkb; kb0 += kGroup) {
-                bool ok = mbar_wait_polls(at(&s.scale_full[c.slot]), c.parity);
+                ok = mbar_wait_polls(at(&s.scale_full[c.slot]), c.parity) && ok;
                 const float *f0 = &s.scales[c.slot][0][quarter * 32 + lane];
                 if (kb0 == 0) tile = s.tile[c.slot];
 #pragma unroll
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         tmem_wait_load(r);
                         if (k == kHalves * 4 - 1) {   // all read: the accumulator is free
                             tcgen05_fence_before();
-                            if (kCtas == 2) mbar_arrive_first(at(&s.acc_empty[i]), issue);
+                            if (kCtas == 2) mbar_arrive_cluster(first_empty + i * 8, issue);
                             else mbar_arrive(at(&s.acc_empty[i]), issue);
                         }
 #pragma unroll
@@ -480,9 +482,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 __syncwarp();
                 mbar_arrive(at(&s.scale_empty[c.slot]), issue);
                 c.advance(kScaleSlots);
-                go = __all_sync(0xffffffffu, ok);
-                if (!go) break;
+                if (!ok) break;   // the lanes of a warp poll together and see the same
             }
+            go = __all_sync(0xffffffffu, ok);
             if (!go) break;
             const int nrows = min(tile.y - quarter * 32, 32);   // rows of this warp
             const int n0 = tile.z + wg * kFirst;                // first column

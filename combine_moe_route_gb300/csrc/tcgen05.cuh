@@ -230,15 +230,22 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes, bool i
         : "memory");
 }
 
-// Arrives on the barrier at this place in the first block of the cluster.
-// Relaxed: what it orders are reads of tensor memory, behind tcgen05 fences (a
-// release at cluster scope took about 900 cycles, twice a stage's products).
-__device__ __forceinline__ void mbar_arrive_first(uint32_t bar, bool issue) {
+// The address, for the cluster, of a place of this block's shared memory in the
+// cluster's first block.
+__device__ __forceinline__ uint32_t first_block_address(uint32_t p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(p));
+    return a;
+}
+
+// Arrives on a barrier by such an address.  Relaxed: what it orders are reads of
+// tensor memory, behind tcgen05 fences (a release at cluster scope took about
+// 900 cycles, twice a stage's products).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, bool issue) {
     asm volatile(
-        "{\n\t.reg .b32 a;\n\t.reg .pred q;\n\t"
+        "{\n\t.reg .pred q;\n\t"
         "setp.ne.b32 q, %1, 0;\n\t"
-        "mapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar),
+        "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
         "r"((uint32_t)issue)
         : "memory");
 }

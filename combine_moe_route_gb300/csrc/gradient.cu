@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kGateThreads) gated_backward_kernel(const __nv
         unpack_bf16x8(vd[i], d);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float s = sigmoid(g[k]);
+            const float s = sigmoid_fast(g[k]);
             const float ds = d[k] * s;
             const float du = ds * g[k];
             g[k] = ds * u[k] * __fmaf_rn(g[k], 1.0f - s, 1.0f);

@@ -50,11 +50,15 @@ __device__ __forceinline__ float e4m3_to_float(unsigned char b) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
 }
 
-// The logistic function with __expf and the fast division: within
-// (1 - s) * (2 + 1.2 |v|) + 2 ulp, so a few ulp wherever s is not tiny (expf and
-// an IEEE division made the gates' passes wait on arithmetic).  For v -> -inf,
-// __expf overflows to inf and the result is 0.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+// The logistic function, with expf and the fast division (each within 2 ulp; an
+// IEEE division took the gated product's tiles 10 % longer).  For v -> -inf,
+// expf overflows to inf and the result is 0.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+
+// With __expf: within (1 - s) * (2 + 1.2 |v|) + 2 ulp, a few ulp wherever s is
+// not tiny, for the gate's gradient, which waited on the arithmetic of expf (745
+// against 663 us) and has no forward values to agree with code by code.
+__device__ __forceinline__ float sigmoid_fast(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
 // Pairs of fp32 in one instruction each, rounded as the single operations are.
 __device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {

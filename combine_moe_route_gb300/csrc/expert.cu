@@ -3,10 +3,9 @@
 // that owns the row (s_e = 1 in identity mode); xhat is the received bf16
 // value, or the e4m3 value times its per-128-channel scale.
 //
-// The grouped GEMM itself is not part of this library (the sources run it
-// with DeepGEMM; Perplexity, "Lower latency and higher throughput with
-// multi-node DeepSeek deployment", section "GroupGEMM").  This kernel only
-// gives combine deterministic, expert-dependent inputs.
+// The experts' products are in expert_gemm.cu.  This kernel gives combine
+// deterministic, expert-dependent inputs that are exact in bf16 arithmetic, for
+// checking and timing dispatch and combine alone.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

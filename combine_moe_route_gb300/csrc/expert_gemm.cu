@@ -10,11 +10,14 @@
 // outer sum adds that accumulator, times the two scales, to registers.
 //
 // A persistent block per SM walks output tiles of 128 rows of one expert x kBN
-// columns.  Its warps have fixed jobs:
+// columns; for experts of many rows a pair of blocks walks tiles of 256 rows,
+// each holding half of the rows and loading half of the weight's columns (32 KB
+// a stage and block instead of 48).  The warps of a block have fixed jobs:
 //   warp 8      loads the e4m3 tiles of both operands, 128 channels a stage,
 //               with tiled bulk tensor copies into a ring of stages;
-//   warps 9, 10 issue the products of a stage (4 x K = 32 each, 128 columns)
-//               into the tensor memory's accumulators, four in turn;
+//   warps 9, 10 take turns at issuing the products of a stage (4 x K = 32) into
+//               the tensor memory's accumulators, which alternate (two of 256
+//               columns, four of 128);
 //   warp 11     forms the products of the two scales, one per row, channel block
 //               and 128 columns, some blocks ahead, in a ring of its own (reading
 //               them where they are used stalled the sums on L2), and tells the
@@ -36,6 +39,13 @@
 // projection as one tile of 256: each warpgroup holds 64 of both, forms
 // silu(g) * u in fp32, and the two exchange their maxima of a row to quantise
 // its block of 128.
+//
+// What bounds it: few rows, the weight's bytes (256 experts x 32 rows, 7168 x
+// 2048: 3.9 GB in 570 us, 0.99 of the measured copy rate).  Many rows, the
+// tensor cores (75 % of the cycles) and the power they draw: 8 experts x 1024
+// rows, 4096 x 7168, in 158 us (3.0 PFLOP/s), 64 experts of them for seconds at
+// 2.8 PFLOP/s, gated, with the SM clock at 1.52 GHz.  A stage takes about 650
+// cycles of which its products are 512; the sums alone would take about 600.
 #include <atomic>
 
 #include "launch.h"
@@ -645,7 +655,11 @@ static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cud
 
 template <bool kTransposed, bool kGated>
 static cudaError_t launch_product(const void *a, const void *w, ProductArgs p, cudaStream_t stream) {
-    // pairs where an expert has more than a single block's rows on average
+    // Pairs where an expert has more than a single block's rows on average.  64 experts, 7168 x
+    // 2048, rows each: 128: 202 us in pairs, 160 in single blocks; 160: 205 and 236; 256: 212 and
+    // 231; 320: pairs alone 395, single blocks 320, pairs and tails 352.  256 experts, 262144
+    // rows: pairs and tails 3.56 ms, pairs alone 3.62, single blocks 3.75; 65536 rows, transposed,
+    // 4096 to 7168: 2.24, 2.48 and 2.36 ms.
     if (p.rows > (long long)p.E * kRowTile) {
         const cudaError_t e = launch_tiles<2, 256, kTransposed, kGated>(a, w, p, stream);
         if (e != cudaSuccess) return e;
@@ -653,8 +667,8 @@ static cudaError_t launch_product(const void *a, const void *w, ProductArgs p, c
         return launch_tiles<1, 256, kTransposed, kGated>(a, w, p, stream);
     }
     if constexpr (!kGated) {
-        // tiles of 256 columns read A half as often; where they are few, 128 columns spread over
-        // more SMs
+        // tiles of 256 columns read A half as often (64 experts x 8 rows, 4096 to 7168 transposed:
+        // 270 us, with 128 columns 285); where they are few, 128 columns spread over more SMs
         const long long tiles = ((long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E)) * ((p.N + 255) / 256);
         if (tiles < 4 * device_sm_count()) return launch_tiles<1, 128, kTransposed, kGated>(a, w, p, stream);
     }

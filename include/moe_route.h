@@ -247,8 +247,9 @@ MOE_API moe_status moe_dispatch_noalloc(const void *x, const int32_t *topk_idx,
                                         int32_t *tok2row, int32_t *row2src, moe_stream_t stream);
 
 /*
- * moe_expert_scale -- stand-in for the grouped expert GEMM (which is not part
- * of this library): y[row] = bf16(xhat * s_e) with s_e = 1 + e/256 for the
+ * moe_expert_scale -- stand-in for the experts' products (moe_expert_gemm and
+ * moe_expert_gated_gemm below), deterministic and exact, for checking and timing
+ * dispatch and combine alone: y[row] = bf16(xhat * s_e) with s_e = 1 + e/256 for the
  * expert e whose rows [expert_offsets[e], expert_offsets[e+1]) hold `row`
  * (s_e = 1 when identity != 0); xhat is the bf16 value, or for an FP8 buffer
  * e4m3 value * recv_scale (one fp32 multiply).

@@ -76,6 +76,7 @@ struct ProductArgs {
     int E, N, C;
     int rows;
     int ntiles;         // column tiles
+    int split;          // blocks that share a tile's channels (split launches)
     bool tails;         // single blocks: only what the pairs' launch before leaves (see below)
     bool out_f32;
     void *out;          // plain form: [rows, N]
@@ -177,10 +178,12 @@ __device__ __forceinline__ Tile tile_at(const Shared &s, const ProductArgs &p, l
 // memory, four lanes per row, through the warp's staging, which is swizzled
 // against bank conflicts.  (Each lane writing its own row took three times as
 // long: 32 lines a store.)  `dst` is the address in the warp's row 0, rows lie
-// `pitch` bytes apart; rows at or past nrows and bytes at or past `limit` are
-// not written.
+// `pitch` bytes apart.  `keep`: which rows to write, a bit each (kMask) or the first
+// so many (a mask's bits cost a product's tiles 2 %); bytes at or past `limit`
+// are not written.
+template <bool kMask>
 __device__ __forceinline__ void store_rows64(const uint4 (&v)[4], uint32_t stage, unsigned char *dst, size_t pitch,
-                                             int nrows, int limit, int lane) {
+                                             uint32_t keep, int limit, int lane) {
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c) st_shared_v4(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16), v[c]);
@@ -190,13 +193,15 @@ __device__ __forceinline__ void store_rows64(const uint4 (&v)[4], uint32_t stage
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + (lane >> 2);
         const uint4 x = ld_shared_v4(stage + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
-        if (r < nrows && c * 16 < limit) st_v4(dst + (size_t)r * pitch + c * 16, x);
+        const bool kept = kMask ? (keep >> r & 1u) != 0 : r < (int)keep;
+        if (kept && c * 16 < limit) st_v4(dst + (size_t)r * pitch + c * 16, x);
     }
 }
 
 // 64 fp32 values of a row, as bf16.
+template <bool kMask>
 __device__ __forceinline__ void store_bf16x64(const float2 *acc, uint32_t stage, unsigned char *dst, size_t pitch,
-                                              int nrows, int limit, int lane) {
+                                              uint32_t keep, int limit, int lane) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         uint4 v[4];
@@ -206,11 +211,14 @@ __device__ __forceinline__ void store_bf16x64(const float2 *acc, uint32_t stage,
             v[i] = make_uint4(bf16_pair(a[0].x, a[0].y), bf16_pair(a[1].x, a[1].y), bf16_pair(a[2].x, a[2].y),
                               bf16_pair(a[3].x, a[3].y));
         }
-        store_rows64(v, stage, dst + c * 64, pitch, nrows, limit - c * 64, lane);
+        store_rows64<kMask>(v, stage, dst + c * 64, pitch, keep, limit - c * 64, lane);
     }
 }
 
-template <int kCtas, int kBN, bool kTransposed, bool kGated>
+// kSplit: the blocks of a cluster share one tile, each taking a run of its
+// channels, and then add up: a row's sums go to the block that owns the row,
+// through the shared memory of its ring, which is free by then.
+template <int kCtas, int kBN, bool kTransposed, bool kGated, bool kSplit>
 __global__ void __launch_bounds__(kProductThreads, 1)
     expert_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_few,
                           const __grid_constant__ CUtensorMap map_w, const ProductArgs p) {
@@ -223,6 +231,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const bool issue = lane == 0;
     const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
     const int nkb = (p.C + kBlockK - 1) / kBlockK;
+    const int parts = kSplit ? p.split : 1, part = kSplit ? (int)cluster_rank() : 0;
+    const int kb_first = kSplit ? nkb * part / parts : 0;                     // this block's channels
+    const int nk = kSplit ? nkb * (part + 1) / parts - kb_first : nkb;
 
     // prologue: barriers, tensor memory, and the experts' row tiles
     if (threadIdx.x == 0) {
@@ -306,7 +317,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             // ---------------------------------------------------- loads
             Ring r;
             long long issued = 0;
-            for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
+            for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += kSplit ? total : gridDim.x / kCtas) {
                 const Tile tile = tile_at<kCtas>(s, p, t, rank);
                 const int n0 = tile.n * (kGated ? kBN / 2 : kBN);
                 // a pair splits the columns: each block brings half of them
@@ -319,7 +330,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     (kCtas == 2 ? row_load_bytes(min(tile.pair_valid, kRowTile)) +
                                       row_load_bytes(tile.pair_valid - kRowTile)
                                 : row_load_bytes(tile.valid));
-                for (int kb = 0; kb < nkb; ++kb) {
+                for (int kb = kb_first; kb < kb_first + nk; ++kb) {
                     go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.empty[r.slot]), r.parity ^ 1u));
                     if (!go) break;
                     const uint32_t a = tiles_at + r.slot * Layout::kStageBytes, w = a + kStageA;
@@ -366,8 +377,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const uint64_t w0 = smem_descriptor(tiles_at + kStageA, kTransposed ? 128 * kBlockK : 16, 1024);
                 Ring r;
                 uint32_t parities = 0;   // of the accumulators' passes
-                for (long long t = blockIdx.x; go && t < total * kCtas; t += gridDim.x) {
-                    for (int kb = 0; kb < nkb; ++kb) {
+                for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += kSplit ? total : gridDim.x / kCtas) {
+                    for (int kb = 0; kb < nk; ++kb) {
                         if ((kb & 1) == turn) {
                             const int slot = kb % Layout::kGroup;
                             const bool free_now =
@@ -399,7 +410,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const int nb = (p.N + 127) / 128;           // scale blocks along the columns
             const size_t step = kTransposed ? nb : 1;   // from one block of channels to the next
             Ring c;
-            for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
+            for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += kSplit ? total : gridDim.x / kCtas) {
                 const Tile tile = tile_at<kCtas>(s, p, t, rank);
                 const float *sw[Layout::kHalves];
 #pragma unroll
@@ -408,11 +419,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     const int block = kGated ? h * (nb / 2) + tile.n : min(tile.n * Layout::kHalves + h, nb - 1);
                     sw[h] = p.w_scale + (size_t)tile.e * nkb * nb + (kTransposed ? (size_t)block : (size_t)block * nkb);
                 }
-                for (int kb0 = 0; kb0 < nkb; kb0 += Layout::kGroup) {
+                for (int kb0 = 0; kb0 < nk; kb0 += Layout::kGroup) {
                     float fa[4][Layout::kGroup], fw[Layout::kHalves][Layout::kGroup];
 #pragma unroll
                     for (int i = 0; i < Layout::kGroup; ++i) {
-                        const int kb = min(kb0 + i, nkb - 1);
+                        const int kb = kb_first + min(kb0 + i, nk - 1);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int r = q * 32 + lane;
@@ -437,6 +448,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 }
             }
         }
+        if (kSplit) {   // the sums' exchange below
+            cluster_barrier();
+            cluster_barrier();
+        }
     } else {
         // ------------------------------------- scaled sums and the output
         registers_increase<kSumRegisters>();
@@ -451,19 +466,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint32_t first_empty = kCtas == 2 ? first_block_address(at(&s.acc_empty[0])) : 0;   // 8 bytes each
         Ring c;
         uint32_t parities = 0, pair_parity = 0;
-        for (long long t = blockIdx.x / kCtas; go && t < total; t += gridDim.x / kCtas) {
+        for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += kSplit ? total : gridDim.x / kCtas) {
             int4 tile;
             float2 acc[kHalves * 32];
 #pragma unroll
             for (int i = 0; i < kHalves * 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
             bool ok = true;
-            for (int kb0 = 0; kb0 < nkb; kb0 += kGroup) {
+            for (int kb0 = 0; kb0 < nk; kb0 += kGroup) {
                 ok = mbar_wait_polls(at(&s.scale_full[c.slot]), c.parity) && ok;
                 const float *f0 = &s.scales[c.slot][0][quarter * 32 + lane];
                 if (kb0 == 0) tile = s.tile[c.slot];
 #pragma unroll
                 for (int i = 0; i < kGroup; ++i) {
-                    if (i > 0 && kb0 + i >= nkb) break;
+                    if (i > 0 && kb0 + i >= nk) break;
                     float f[kHalves];   // read here: a read after the wait would wait in its turn
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h)
@@ -495,17 +510,52 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (!ok) break;   // the lanes of a warp poll together and see the same
             }
             go = __all_sync(0xffffffffu, ok);
+            uint32_t keep;   // rows of this warp that are this block's to write: a mask (kSplit) or how many
+            if constexpr (kSplit) {
+                const int row = quarter * 32 + lane, owner = row % parts;
+                const bool valid = go && row < tile.y;
+                constexpr int kRowBytes = kBN * 4 + 16;   // no bank conflicts between rows
+                // part q's sums of the owner's rows, one after the other
+                const auto room = [&](int q) {
+                    return tiles_at + (q * (kRowTile / parts) + row / parts) * kRowBytes + wg * kBN * 2;
+                };
+                cluster_barrier();   // every block's products are done with its ring
+                if (valid && owner != part) {
+                    const uint32_t to = block_address(room(part), owner);
+#pragma unroll
+                    for (int i = 0; i < kHalves * 16; ++i)
+                        st_cluster_v4(to + i * 16, make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x,
+                                                               acc[2 * i + 1].y));
+                }
+                cluster_barrier();
+                if (valid && owner == part) {
+                    for (int q = 0; q < parts; ++q) {   // ascending, after the own: an order that never changes
+                        if (q == part) continue;
+                        const uint32_t from = room(q);
+#pragma unroll
+                        for (int i = 0; i < kHalves * 16; ++i) {
+                            const uint4 v = ld_shared_v4(from + i * 16);
+                            acc[2 * i].x += __uint_as_float(v.x);
+                            acc[2 * i].y += __uint_as_float(v.y);
+                            acc[2 * i + 1].x += __uint_as_float(v.z);
+                            acc[2 * i + 1].y += __uint_as_float(v.w);
+                        }
+                    }
+                }
+                keep = __ballot_sync(0xffffffffu, valid && owner == part);
+            } else {
+                keep = (uint32_t)max(min(tile.y - quarter * 32, 32), 0);
+            }
             if (!go) break;
-            const int nrows = min(tile.y - quarter * 32, 32);   // rows of this warp
             const int n0 = tile.z + wg * kFirst;                // first column
-            const bool mine = nrows > 0 && n0 < p.N;
+            const bool mine = keep != 0 && n0 < p.N;
             const size_t warp_row = (size_t)tile.x + quarter * 32;
             if constexpr (kGated) {
                 const int I = p.N / 2;
                 if (p.h && mine) {
                     unsigned char *h = reinterpret_cast<unsigned char *>(p.h + warp_row * p.N + n0);
-                    store_bf16x64(acc, stage, h, (size_t)p.N * 2, nrows, 128, lane);
-                    store_bf16x64(acc + 32, stage, h + (size_t)I * 2, (size_t)p.N * 2, nrows, 128, lane);
+                    store_bf16x64<kSplit>(acc, stage, h, (size_t)p.N * 2, keep, 128, lane);
+                    store_bf16x64<kSplit>(acc + 32, stage, h + (size_t)I * 2, (size_t)p.N * 2, keep, 128, lane);
                 }
                 float amax = 0.0f;
 #pragma unroll
@@ -537,8 +587,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         }
                         v[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    store_rows64(v, stage, p.q + warp_row * I + n0, I, nrows, 64, lane);
-                    if (wg == 0 && lane < nrows)
+                    store_rows64<kSplit>(v, stage, p.q + warp_row * I + n0, I, keep, 64, lane);
+                    if (wg == 0 && (kSplit ? (keep >> lane & 1u) != 0 : lane < (int)keep))
                         p.q_scale[(warp_row + lane) * (I / 128) + n0 / 128] = quant_scale(amax);
                 }
             } else if (mine) {
@@ -546,9 +596,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 for (int h = 0; h < kHalves; ++h) {
                     const int n = n0 + h * 64;
                     if (!p.out_f32) {
-                        store_bf16x64(acc + h * 32, stage,
+                        store_bf16x64<kSplit>(acc + h * 32, stage,
                                       static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 2, (size_t)p.N * 2,
-                                      nrows, (p.N - n) * 2, lane);
+                                      keep, (p.N - n) * 2, lane);
                         continue;
                     }
 #pragma unroll
@@ -560,12 +610,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                             v[i] = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
                                               __float_as_uint(v1.y));
                         }
-                        store_rows64(v, stage,
+                        store_rows64<kSplit>(v, stage,
                                      static_cast<unsigned char *>(p.out) + (warp_row * p.N + n + c * 16) * 4,
-                                     (size_t)p.N * 4, nrows, (p.N - n) * 4 - c * 64, lane);
+                                     (size_t)p.N * 4, keep, (p.N - n) * 4 - c * 64, lane);
                     }
                 }
             }
+        }
+        if (kSplit && blockIdx.x / parts >= total) {   // no tile: the exchange is the cluster's all the same
+            cluster_barrier();
+            cluster_barrier();
         }
     }
     if (!go && issue) atomicOr(&g_product_error, MOE_DEVERR_COPY_TIMEOUT);
@@ -612,14 +666,14 @@ static bool encode_bytes(CUtensorMap *map, const void *base, uint64_t x, uint64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kCtas, int kBN, bool kTransposed, bool kGated>
+template <int kCtas, int kBN, bool kTransposed, bool kGated, bool kSplit = false>
 static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cudaStream_t stream) {
     CUtensorMap map_a, map_few, map_w;
     if (!encode_bytes(&map_a, a, p.C, p.rows, 0, kRowTile) || !encode_bytes(&map_few, a, p.C, p.rows, 0, kFewRows) ||
         !encode_bytes(&map_w, w, kTransposed ? p.N : p.C, kTransposed ? p.C : p.N, p.E,
                       kTransposed ? kBlockK : weight_box<kCtas, kBN, kTransposed, kGated>()))
         return cudaErrorInvalidValue;
-    auto kernel = expert_product_kernel<kCtas, kBN, kTransposed, kGated>;
+    auto kernel = expert_product_kernel<kCtas, kBN, kTransposed, kGated, kSplit>;
     constexpr int smem = ProductLayout<kCtas, kBN>::kBytes;
     static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
     int dev = 0;
@@ -638,19 +692,33 @@ static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cud
                            p.ntiles;
     const int groups = device_sm_count() / kCtas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(kCtas * (most < groups ? (most > 0 ? most : 1) : groups)));
+    const int parts = kSplit ? p.split : 1;
+    cfg.gridDim = dim3((unsigned)(kSplit ? most * parts : kCtas * (most < groups ? (most > 0 ? most : 1) : groups)));
     cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.x = kSplit ? parts : kCtas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, map_a, map_few, map_w, p);
+}
+
+// Into how many parts a tile's channels are split so that few tiles use the
+// card: at least four stages each, and no more clusters than fit at once (of 152
+// SMs, 15 clusters of eight, 36 of four, 76 of two).  2 experts x 8 rows, gated,
+// 2 x 2048 x 7168, 32 tiles: 22.5 us in one part, 16.2 in two, 13.3 in four; one
+// expert: 22.4 and in eight 12.2.
+static int split_parts(long long tiles, int C) {
+    const int stages = (C + kBlockK - 1) / kBlockK;
+    for (int parts = 8; parts > 1; parts /= 2)
+        if (tiles * parts <= device_sm_count() * (parts == 8 ? 0.79 : parts == 4 ? 0.95 : 1.0) && stages >= 4 * parts)
+            return parts;
+    return 1;
 }
 
 template <bool kTransposed, bool kGated>
@@ -666,11 +734,15 @@ static cudaError_t launch_product(const void *a, const void *w, ProductArgs p, c
         p.tails = true;
         return launch_tiles<1, 256, kTransposed, kGated>(a, w, p, stream);
     }
+    const long long row_tiles = (long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E);   // at most
+    constexpr int kNarrow = kGated ? 256 : 128;
+    p.split = split_parts(row_tiles * ((p.N + kNarrow - 1) / kNarrow), p.C);
+    if (p.split > 1) return launch_tiles<1, kNarrow, kTransposed, kGated, true>(a, w, p, stream);
     if constexpr (!kGated) {
         // tiles of 256 columns read A half as often (64 experts x 8 rows, 4096 to 7168 transposed:
         // 270 us, with 128 columns 285); where they are few, 128 columns spread over more SMs
-        const long long tiles = ((long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E)) * ((p.N + 255) / 256);
-        if (tiles < 4 * device_sm_count()) return launch_tiles<1, 128, kTransposed, kGated>(a, w, p, stream);
+        if (row_tiles * ((p.N + 255) / 256) < 4 * device_sm_count())
+            return launch_tiles<1, 128, kTransposed, kGated>(a, w, p, stream);
     }
     return launch_tiles<1, 256, kTransposed, kGated>(a, w, p, stream);
 }

@@ -230,12 +230,18 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes, bool i
         : "memory");
 }
 
-// The address, for the cluster, of a place of this block's shared memory in the
-// cluster's first block.
-__device__ __forceinline__ uint32_t first_block_address(uint32_t p) {
+// The address, for the cluster, of a place of this block's shared memory in
+// another of its blocks.
+__device__ __forceinline__ uint32_t block_address(uint32_t p, uint32_t rank) {
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(p));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(p), "r"(rank));
     return a;
+}
+__device__ __forceinline__ uint32_t first_block_address(uint32_t p) { return block_address(p, 0); }
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t p, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
 }
 
 // Arrives on a barrier by such an address.  Relaxed: what it orders are reads of

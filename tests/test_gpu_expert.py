@@ -62,6 +62,38 @@ def test_product_long_contraction(gpu, C, transpose):
     assert float((o - want).norm() / want.norm()) < 1e-6
 
 
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("C", [512, 1040, 2048, 4112, 7168])
+@pytest.mark.parametrize("counts", [[1], [3, 0, 1], [33], [70, 20], [128]])
+def test_few_tiles_over_a_long_contraction(gpu, counts, C, transpose):
+    """Tiles so few that blocks share a tile's channels and add up: 128 and 144 columns over short
+    and long contractions, rows that spread over the blocks and rows that do not; the sums repeat
+    bit for bit."""
+    from combine_moe_route_gb300 import binding as b
+    for N in (128, 144):
+        inp = ref.product_inputs(counts, N, C, np.random.default_rng(C + N), transpose)
+        want, mag = ref.product(inp, transpose)
+        args = _to(gpu, inp)
+        o = b.expert_gemm(*args, transpose=transpose, out_dtype=torch.float32)
+        assert ((o.cpu().double() - want).abs() <= ref.product_bound(mag, C)).all()
+        assert float((o.cpu().double() - want).norm() / want.norm()) < 1e-6
+        o16 = b.expert_gemm(*args, transpose=transpose)
+        assert torch.equal(o16, o.bfloat16())
+        for _ in range(3):
+            assert torch.equal(b.expert_gemm(*args, transpose=transpose, out_dtype=torch.float32), o)
+    if not transpose and C % 128 == 0:
+        I = 128
+        inp = ref.product_inputs(counts, 2 * I, C, np.random.default_rng(C))
+        p, mag = ref.product(inp)
+        err = ref.product_bound(mag, C)
+        g, u, eg, eu = p[:, :I], p[:, I:], err[:, :I], err[:, I:]
+        v = ref.gate(g, u)
+        verr = 1.1 * eg * (u.abs() + eu) + g.abs() * eu + 8 * 2.0 ** -24 * v.abs()
+        r = b.expert_gated_gemm(*_to(gpu, inp), save_h=True)
+        assert ref.quantized_ok(r.q.cpu(), r.scale.cpu(), v, verr) == (True, True)
+        assert ((r.h.cpu().double() - p).abs() <= err + 2.0 ** -8 * p.abs()).all()
+
+
 @pytest.mark.parametrize("save", [False, True])
 @pytest.mark.parametrize("I,C", [(128, 128), (256, 144), (384, 640), (640, 2048)])
 @pytest.mark.parametrize("name", sorted(COUNTS))

@@ -25,7 +25,8 @@ def hooked(tmp_path_factory):
     return binding.load_library(build.build(out_dir=out, defines=("MOE_TEST_WITHHOLD_PRODUCT_STAGE=1",)))
 
 
-@pytest.mark.parametrize("counts", [[20], [200, 300]])      # single blocks; pairs and a tail of 44 rows
+# blocks that share a tile's channels; single blocks (of many tiles); pairs and a tail of 44 rows
+@pytest.mark.parametrize("counts", [[20], [1] * 100, [200, 300]])
 def test_a_stage_that_never_comes(hooked, counts):
     from combine_moe_route_gb300 import binding as b
     gpu = torch.device("cuda:0")

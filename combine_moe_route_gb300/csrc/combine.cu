@@ -21,6 +21,8 @@
 // of the token sit in shared memory.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "launch.h"
 #include "trace.cuh"
 
@@ -147,7 +149,8 @@ cudaError_t launch_combine(const void *y, const int32_t *tok2row, const float *t
 cudaError_t launch_dispatch_backward(const void *drows, const int32_t *tok2row, int T, int K, int H, long long rows,
                                      bool out_f32, void *dx, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)T * kCombineSplit));
+    constexpr long long kMostBlocks = (1ll << 31) - kCombineSplit;   // the blocks walk what a grid cannot hold
+    cfg.gridDim = dim3((unsigned)std::min((long long)T * kCombineSplit, kMostBlocks));
     cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -40,6 +40,9 @@
 // silu(g) * u in fp32, and the two exchange their maxima of a row to quantise
 // its block of 128.
 //
+// Where the tiles are too few to occupy the card, the blocks of a cluster share
+// a tile's channels (split_parts) and add up through each other's shared memory.
+//
 // What bounds it: few rows, the weight's bytes (256 experts x 32 rows, 7168 x
 // 2048: 3.9 GB in 570 us, 0.99 of the measured copy rate).  Many rows, the
 // tensor cores (75 % of the cycles) and the power they draw: 8 experts x 1024
@@ -711,8 +714,8 @@ static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cud
 // Into how many parts a tile's channels are split so that few tiles use the
 // card: at least four stages each, and no more clusters than fit at once (of 152
 // SMs, 15 clusters of eight, 36 of four, 76 of two).  2 experts x 8 rows, gated,
-// 2 x 2048 x 7168, 32 tiles: 22.5 us in one part, 16.2 in two, 13.3 in four; one
-// expert: 22.4 and in eight 12.2.
+// 2 x 2048 x 7168, 32 tiles: 22.6 us in one part, 16.2 in two, 13.4 in four; one
+// expert: 22.4 and in eight 12.1.
 static int split_parts(long long tiles, int C) {
     const int stages = (C + kBlockK - 1) / kBlockK;
     for (int parts = 8; parts > 1; parts /= 2)

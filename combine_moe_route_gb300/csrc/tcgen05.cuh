@@ -262,8 +262,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-// Every thread of every block of the cluster.
+// Every thread of every block of the cluster; a warp's lanes arrive together.
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

@@ -261,17 +261,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         prefetch_tensor_map(&map_w);
     }
     if (warp == 9) tmem_alloc<kCtas, kTmemColumns>(&s.tmem);
-    // up to here nothing is read: this block may have started while the kernel before ran out,
-    // and lets the kernel after do the same.  The tails' launch reads nothing that the pairs'
-    // writes, so it fills the SMs as those run out: pairs let it start once what came before
-    // them is done, and it waits for them at its own end, for whoever waits for it.
-    if (kCtas == 2) {
-        pdl_wait();
-        pdl_launch_dependents();
-    } else {
-        pdl_launch_dependents();
-        if (!p.tails) pdl_wait();
-    }
+    // Up to here nothing is read: this block may have started while the kernel before ran out, and
+    // lets the kernel after do the same.  Only this wait makes what earlier kernels wrote visible,
+    // so it stands before the first read in the tails' launch as well, although what that reads
+    // was written before the pairs' launch: that the pairs waited for it orders their own reads,
+    // not those of a grid that starts beside them.
+    pdl_launch_dependents();
+    pdl_wait();
     {
         constexpr int kPer = (MOE_MAX_EXPERTS + kProductThreads - 1) / kProductThreads;
         int mine = 0, mt[kPer];
@@ -632,7 +628,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     else __syncthreads();
     tcgen05_fence_after();
     if (warp == 9) tmem_free<kCtas, kTmemColumns>(tmem);
-    if (kCtas == 1 && p.tails) pdl_wait();
 }
 
 // ------------------------------------------------------------------- host

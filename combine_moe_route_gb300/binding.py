@@ -6,6 +6,9 @@ streams.  Functions keep the C names without the ``moe_`` prefix; each checks
 shapes, dtypes and devices, allocates outputs that were not passed in (with
 torch, on the input's device), and calls the matching C entry point on the
 current torch stream (or the one given).  A non-OK status raises ``MoeError``.
+Outputs come from the current stream's memory: with another ``stream`` given, hold
+inputs and outputs until that stream is past them (or ``record_stream`` it), and order
+it behind the current stream first; ``experts`` does both for its own tensors.
 
 There is no CPU fallback: if the library is missing, loading raises
 ``ImportError``; if the tensors are not on a CUDA device, ``ValueError``.

@@ -12,7 +12,7 @@ pass gradients through unchanged.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, fields, is_dataclass
 
 import torch
 
@@ -60,33 +60,68 @@ class ExpertForward:
     y: torch.Tensor                     # [T*K, H] bf16: the expert outputs
 
 
+def _record(stream, *values) -> None:
+    """Every tensor in ``values`` (in results and weights too) keeps its memory, once dropped, until
+    what ``stream`` has been given by then is done."""
+    for v in values:
+        if is_dataclass(v):
+            _record(stream, *(getattr(v, f.name) for f in fields(v)))
+        elif isinstance(v, tuple):
+            _record(stream, *v)
+        elif getattr(v, "is_cuda", False):   # anything else is the bindings' to refuse
+            v.record_stream(stream)
+
+
+def _on(stream, inputs: tuple, run):
+    """``run()`` with ``stream`` current (None: as it is), so that what a pass allocates belongs to the
+    stream that it runs on: its temporaries are dropped while the stream has yet to reach them.  The
+    inputs come from the caller's stream and the results go there; each may be dropped while the
+    other stream still uses it."""
+    if stream is None:
+        return run()
+    caller = torch.cuda.current_stream(stream.device)
+    _record(stream, *inputs)
+    with torch.cuda.stream(stream):
+        result = run()
+    _record(caller, result)
+    return result
+
+
 def expert_layer(x: torch.Tensor, logits: torch.Tensor, B, K: int, weights: ExpertWeights, *, train: bool = False,
                  out_dtype: torch.dtype = torch.bfloat16, stream=None) -> ExpertForward:
     """One layer: x [T, H] bf16 and logits [T, E] fp32 to the combined [T, H].  ``train`` keeps the
-    pre-activations for ``expert_layer_backward``.  Everything is enqueued, nothing synchronises."""
+    pre-activations for ``expert_layer_backward``.  Everything is enqueued on ``stream`` (default: the
+    current one), nothing synchronises: a given stream has to be ordered behind the work that writes
+    the inputs, and whoever reads the results behind the stream."""
     E = weights.E
-    idx, w = _b.route_topk(logits, K, stream=stream)
-    d = _b.dispatch(x, idx, B, E, fp8=True, stream=stream)
-    g = _b.expert_gated_gemm(d.recv_x, d.recv_scale, weights.w13, weights.w13_scale, d.expert_offsets, save_h=train,
-                             stream=stream)
-    y = _b.expert_gemm(g.q, g.scale, weights.w2, weights.w2_scale, d.expert_offsets, stream=stream)
-    out = _b.combine(y, d.tok2row, w, out_dtype=out_dtype, stream=stream)
-    return ExpertForward(out, idx, w, d, g, y)
+
+    def run():
+        idx, w = _b.route_topk(logits, K)
+        d = _b.dispatch(x, idx, B, E, fp8=True)
+        g = _b.expert_gated_gemm(d.recv_x, d.recv_scale, weights.w13, weights.w13_scale, d.expert_offsets,
+                                 save_h=train)
+        y = _b.expert_gemm(g.q, g.scale, weights.w2, weights.w2_scale, d.expert_offsets)
+        out = _b.combine(y, d.tok2row, w, out_dtype=out_dtype)
+        return ExpertForward(out, idx, w, d, g, y)
+
+    return _on(stream, (x, logits, weights), run)
 
 
 def expert_layer_backward(dout: torch.Tensor, fwd: ExpertForward, weights: ExpertWeights, *, stream=None):
-    """(dx [T, H] bf16, dlogits [T, E] fp32) for dout [T, H] bf16 and a ``train`` forward."""
+    """(dx [T, H] bf16, dlogits [T, E] fp32) for dout [T, H] bf16 and a ``train`` forward; ``stream`` as
+    there."""
     if fwd.gated.h is None:
         raise ValueError("the forward pass kept no pre-activations: run it with train=True")
     d, K = fwd.dispatch, fwd.topk_idx.shape[1]
-    c = _b.combine_backward(dout, fwd.y, d.tok2row, fwd.topk_w, topk_idx=fwd.topk_idx, E=weights.E, fp8=True,
-                            stream=stream)
-    dv = _b.expert_gemm(c.dy, c.dy_scale, weights.w2, weights.w2_scale, d.expert_offsets, transpose=True,
-                        stream=stream)
-    dh, dh_scale = _b.expert_gated_backward(fwd.gated.h, dv, stream=stream)
-    drows = _b.expert_gemm(dh, dh_scale, weights.w13, weights.w13_scale, d.expert_offsets, transpose=True,
-                           stream=stream)
-    return _b.dispatch_backward(drows, d.tok2row, K, stream=stream), c.dlogits
+
+    def run():
+        c = _b.combine_backward(dout, fwd.y, d.tok2row, fwd.topk_w, topk_idx=fwd.topk_idx, E=weights.E, fp8=True)
+        dv = _b.expert_gemm(c.dy, c.dy_scale, weights.w2, weights.w2_scale, d.expert_offsets, transpose=True)
+        dh, dh_scale = _b.expert_gated_backward(fwd.gated.h, dv)
+        drows = _b.expert_gemm(dh, dh_scale, weights.w13, weights.w13_scale, d.expert_offsets, transpose=True)
+        return _b.dispatch_backward(drows, d.tok2row, K), c.dlogits
+
+    return _on(stream, (dout, fwd, weights), run)
 
 
 def main() -> None:

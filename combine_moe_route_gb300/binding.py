@@ -831,8 +831,8 @@ def expert_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w
 
 
 def get_expert_error(device=None, stream=None) -> tuple[int, int]:
-    """Synchronise the stream, read and clear the device's error word of the expert products:
-    (status, raw bits)."""
+    """Synchronise the stream, read and clear the device's error word of the expert products, which
+    all of its streams share: (status, raw bits)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     code = ctypes.c_int32(0)
     with torch.cuda.device(dev):

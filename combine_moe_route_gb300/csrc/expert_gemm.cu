@@ -49,6 +49,8 @@
 // rows, 4096 x 7168, in 158 us (3.0 PFLOP/s), 64 experts of them for seconds at
 // 2.8 PFLOP/s, gated, with the SM clock at 1.52 GHz.  A stage takes about 650
 // cycles of which its products are 512; the sums alone would take about 600.
+#include <pthread.h>
+
 #include <atomic>
 
 #include "launch.h"
@@ -70,8 +72,9 @@ constexpr int kStagingWarp = 32 * 64;       // output staging of a warp: 32 rows
 constexpr int kScaleSlots = 4;             // of the ring of scales
 constexpr int kTmemColumns = 512;
 
-// Set when a bounded wait of a product kernel ran out (never in a sound run).
-__device__ int32_t g_product_error;
+// Set when a bounded wait of a product kernel ran out (never in a sound run), and
+// what the last read took out of it.
+__device__ int32_t g_product_error, g_product_error_taken;
 
 struct ProductArgs {
     const float *a_scale, *w_scale;
@@ -765,17 +768,26 @@ cudaError_t launch_expert_gated_gemm(const void *a, const float *a_scale, const 
     return launch_product<false, true>(a, w, p, stream);
 }
 
+// Read and cleared in one step: a product on another stream whose wait runs out
+// meanwhile is either in this read or in the next.
+__global__ void take_product_error_kernel() { g_product_error_taken = atomicExch(&g_product_error, 0); }
+
 cudaError_t read_product_error(int32_t *host_code, cudaStream_t stream) {
-    int32_t v = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_product_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    *host_code = 0;
+    cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return e;
-    *host_code = v;
-    if (v) {
-        const int32_t zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_product_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    }
+    // one reader at a time between the exchange and the copy of what it took
+    static pthread_mutex_t reading = PTHREAD_MUTEX_INITIALIZER;
+    pthread_mutex_lock(&reading);
+    take_product_error_kernel<<<1, 1, 0, stream>>>();
+    e = cudaGetLastError();
+    int32_t v = 0;
+    if (e == cudaSuccess)
+        e = cudaMemcpyFromSymbolAsync(&v, g_product_error_taken, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+    const cudaError_t done = cudaStreamSynchronize(stream);   // v is written before this returns, whatever e is
+    pthread_mutex_unlock(&reading);
+    if (e == cudaSuccess) e = done;
+    if (e == cudaSuccess) *host_code = v;
     return e;
 }
 

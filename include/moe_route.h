@@ -538,13 +538,18 @@ MOE_API moe_status moe_expert_gated_gemm(const void *a, const float *a_scale, co
                                          float *q_scale, void *h, moe_stream_t stream);
 
 /*
- * moe_get_expert_error -- SYNCHRONOUS: waits for `stream`, then copies to
- * *host_code and clears the current device's error word of the two products
- * above: MOE_DEVERR_COPY_TIMEOUT once a bounded wait inside one of their
- * kernels has run out (the kernel then returns with its output unspecified),
- * else 0.  Returns MOE_ERR_TIMEOUT, or MOE_OK (MOE_ERR_CUDA if the copy fails,
- * MOE_ERR_INVALID_ARG for a NULL pointer).  The word is the library's own, one
- * per device, so the products need no workspace.
+ * moe_get_expert_error -- SYNCHRONOUS: waits for `stream`, then takes (reads and
+ * clears in one step) the current device's error word of the two products above
+ * into *host_code: MOE_DEVERR_COPY_TIMEOUT once a bounded wait inside one of
+ * their kernels has run out (the kernel then returns with its output
+ * unspecified), else 0.  Returns MOE_ERR_TIMEOUT, or MOE_OK (MOE_ERR_CUDA with
+ * *host_code 0 if the copy fails, as on a stream that is being captured,
+ * MOE_ERR_INVALID_ARG for a NULL pointer).
+ * The word is the library's own, one per device, so the products need no
+ * workspace.  It is that of all streams: a read also takes the time-outs of
+ * products on other streams, and does not wait for those still running; whoever
+ * runs products on several streams waits for all of them before the read and
+ * takes its answer for all of them.
  */
 MOE_API moe_status moe_get_expert_error(int32_t *host_code, moe_stream_t stream);
 

@@ -556,7 +556,8 @@ MOE_API moe_status moe_get_expert_error(int32_t *host_code, moe_stream_t stream)
 /*
  * moe_expert_gated_backward -- gradient of the gate.  With (g, u) the halves of
  * a row of h, s = 1 / (1 + exp(-g)) and dv the gradient of v = silu(g) * u,
- *     dg = dv * u * s * (1 + g * (1 - s)),   du = dv * g * s   (fp32),
+ *     dg = dv * u * s * (1 + g * (1 - s)),   du = dv * g * s   (fp32; an s
+ * below 2^-126, from g = -87.4 on, counts as 0),
  * and dh = [dg, du], in bf16 or quantised per 128 channels by moe_dispatch's
  * rule: the operand of the transposed moe_expert_gemm.
  *

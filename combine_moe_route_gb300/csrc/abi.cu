@@ -18,7 +18,13 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 bool topk_shape_ok(int E, int K) { return E >= 1 && E <= MOE_MAX_EXPERTS && K >= 1 && K <= E && K <= MOE_MAX_TOPK; }
 
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+// A failure is reported here and nowhere else: left as the thread's last error, it would be the
+// next launch's.
+moe_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return MOE_OK;
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+}
 
 // Fill the rank table from host B; false if any B is negative or T*K overflows int32.
 bool build_rank_table(int R, const int32_t *B, int K, moe::RankTable &rt, long long &T) {
@@ -344,7 +350,7 @@ moe_status moe_get_device_error(const void *workspace, int32_t *host_code, moe_s
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaMemcpyAsync(&v, workspace, sizeof(v), cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess) return cuda_status(e);
     *host_code = v;
     if (v & (MOE_DEVERR_SCAN_TIMEOUT | MOE_DEVERR_COPY_TIMEOUT | MOE_DEVERR_RECV_TIMEOUT)) return MOE_ERR_TIMEOUT;
     if (v & (MOE_DEVERR_EXPERT_RANGE | MOE_DEVERR_DUPLICATE)) return MOE_ERR_BAD_ROUTING;

@@ -12,7 +12,13 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+// A failure is reported here and nowhere else: left as the thread's last error, it would be the
+// next launch's.
+moe_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return MOE_OK;
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+}
 
 bool expert_dim_ok(int d, int multiple) { return d >= multiple && d <= MOE_MAX_EXPERT_DIM && d % multiple == 0; }
 
@@ -49,8 +55,8 @@ moe_status moe_expert_gated_gemm(const void *a, const float *a_scale, const void
 
 moe_status moe_get_expert_error(int32_t *host_code, moe_stream_t stream) {
     if (!host_code) return MOE_ERR_INVALID_ARG;
-    if (moe::read_product_error(host_code, (cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
-    return *host_code ? MOE_ERR_TIMEOUT : MOE_OK;
+    const moe_status read = cuda_status(moe::read_product_error(host_code, (cudaStream_t)stream));
+    return *host_code ? MOE_ERR_TIMEOUT : read;
 }
 
 moe_status moe_expert_gated_backward(const void *h, const void *dv, int rows, int I, moe_dtype dh_dtype, void *dh,

@@ -62,6 +62,7 @@ moe_status moe_get_expert_error(int32_t *host_code, moe_stream_t stream) {
 moe_status moe_expert_gated_backward(const void *h, const void *dv, int rows, int I, moe_dtype dh_dtype, void *dh,
                                      float *dh_scale, moe_stream_t stream) {
     if (rows < 0 || I < 8 || I > MOE_MAX_EXPERT_DIM / 2 || I % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if ((long long)rows * I > moe::kGatedBackwardMost) return MOE_ERR_INVALID_ARG;
     if (dh_dtype != MOE_DTYPE_BF16 && dh_dtype != MOE_DTYPE_FP8_E4M3) return MOE_ERR_INVALID_ARG;
     const bool fp8 = dh_dtype == MOE_DTYPE_FP8_E4M3;
     if (fp8 && I % 128 != 0) return MOE_ERR_INVALID_ARG;

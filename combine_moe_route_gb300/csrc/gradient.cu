@@ -195,6 +195,7 @@ cudaError_t launch_combine_backward(const void *dout, const void *y, const int32
 // and an IEEE division per channel 807 us.
 constexpr int kGateThreads = 128;
 constexpr int kGateChunks = 2;   // per thread, all loaded before the first is used
+static_assert(kGatedBackwardMost == ((1ll << 31) - 1) * kGateThreads * kGateChunks * 8, "the channels of a grid");
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kGateThreads) gated_backward_kernel(const __nv_bfloat16 *h,

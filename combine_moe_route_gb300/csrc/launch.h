@@ -77,6 +77,8 @@ cudaError_t launch_expert_gated_gemm(const void *a, const float *a_scale, const 
                                      float *q_scale, void *h, cudaStream_t stream);
 // Reads and clears the expert products' error word (synchronous).
 cudaError_t read_product_error(int32_t *host_code, cudaStream_t stream);
+// rows * I of one call: the 2^31 - 1 blocks of a grid, 2048 channels each.
+constexpr long long kGatedBackwardMost = ((1ll << 31) - 1) * 2048;
 cudaError_t launch_gated_backward(const void *h, const void *dv, long long rows, int I, bool fp8, void *dh,
                                   float *dh_scale, cudaStream_t stream);
 cudaError_t launch_combine_backward(const void *dout, const void *y, const int32_t *tok2row, const float *topk_w,

@@ -563,7 +563,8 @@ MOE_API moe_status moe_get_expert_error(int32_t *host_code, moe_stream_t stream)
  *
  *   h          device bf16 [rows, 2*I], 16-byte aligned.
  *   dv         device bf16 [rows, I], 16-byte aligned.
- *   I          a multiple of 8 (of 128 for FP8) in 8..MOE_MAX_EXPERT_DIM/2.
+ *   I          a multiple of 8 (of 128 for FP8) in 8..MOE_MAX_EXPERT_DIM/2;
+ *              rows * I at most (2^31 - 1) * 2048.
  *   dh_dtype   MOE_DTYPE_BF16 or MOE_DTYPE_FP8_E4M3.
  *   dh         device [rows, 2*I] of dh_dtype, 16-byte aligned: out.
  *   dh_scale   device fp32 [rows, 2*I/128]: out, FP8 only (may be NULL for bf16).

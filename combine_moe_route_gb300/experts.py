@@ -94,6 +94,9 @@ def expert_layer(x: torch.Tensor, logits: torch.Tensor, B, K: int, weights: Expe
     current one), nothing synchronises: a given stream has to be ordered behind the work that writes
     the inputs, and whoever reads the results behind the stream."""
     E = weights.E
+    if len(logits.shape) != 2 or logits.shape[1] != E:
+        raise ValueError(f"logits must be [T, E] with a column for each of the weights' {E} experts, got "
+                         f"{tuple(logits.shape)}")
 
     def run():
         idx, w = _b.route_topk(logits, K)

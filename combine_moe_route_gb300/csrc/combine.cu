@@ -62,8 +62,7 @@ __device__ __forceinline__ void fma_row(float (&acc)[8], float w, const uint4 v)
 // combine receive half's wait kernel; nothing is read before that grid is done.
 // kUnit: every row weighs 1, which makes it the gradient of the dispatch scatter
 // (moe_dispatch_backward); launched like kAfterWait, and lets the kernel after
-// do the same, which takes a launch's start out of a run of short ones (1003
-// tokens, top-8, H = 7168: see launch_dispatch_backward).
+// do the same, as the rest of a layer's backward pass does.
 template <bool kOutF32, bool kAfterWait = false, bool kUnit = false>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __nv_bfloat16 *__restrict__ y,
                                                                   const int32_t *__restrict__ tok2row,
@@ -151,7 +150,8 @@ cudaError_t launch_combine(const void *y, const int32_t *tok2row, const float *t
 }
 
 // The gradient of the dispatch scatter: bound by HBM, 32768 tokens, top-8, H =
-// 7168 (4.23 GB) in 606 us, 6.98 TB/s.
+// 7168 (4.23 GB) in 606 us, 6.98 TB/s; 1003 tokens in 21.3 us.  In a run of such
+// calls the early start gains nothing by itself (21.2 us without).
 cudaError_t launch_dispatch_backward(const void *drows, const int32_t *tok2row, int T, int K, int H, long long rows,
                                      bool out_f32, void *dx, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};

@@ -509,6 +509,8 @@ MOE_API moe_status moe_combine_recv(const void *y, const int32_t *tok2row, const
  *                            * sum_{c in b} a[r, c] * w[e, n, c]
  *              (w_scale[e, b, n/128] and w[e, c, n] with transpose), all sums
  *              in fp32, rounded once.  Rows no expert owns are not written.
+ *              The two scales are multiplied first: their product has to be
+ *              finite, and below 2^-126 it is rounded to a multiple of 2^-149.
  * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.
  */
 MOE_API moe_status moe_expert_gemm(const void *a, const float *a_scale, const void *w, const float *w_scale,

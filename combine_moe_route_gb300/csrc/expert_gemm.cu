@@ -44,11 +44,13 @@
 // a tile's channels (split_parts) and add up through each other's shared memory.
 //
 // What bounds it: few rows, the weight's bytes (256 experts x 32 rows, 7168 x
-// 2048: 3.9 GB in 570 us, 0.99 of the measured copy rate).  Many rows, the
-// tensor cores (75 % of the cycles) and the power they draw: 8 experts x 1024
-// rows, 4096 x 7168, in 158 us (3.0 PFLOP/s), 64 experts of them for seconds at
-// 2.8 PFLOP/s, gated, with the SM clock at 1.52 GHz.  A stage takes about 650
-// cycles of which its products are 512; the sums alone would take about 600.
+// 2048: 3.9 GB in 567 us, 0.99 of the measured copy rate).  Many rows, a stage
+// takes about 650 cycles of which its products are 512 (the sums alone would take
+// about 600), and a tile's output about 3000 more, which nothing overlaps: the
+// tensor cores are active 75 % of the cycles over 7168 channels (8 experts x 1024
+// rows, 4096 x 7168, in 157 us, 3.1 PFLOP/s) and 58 % over 2048 (7168 x 2048, 95 us,
+// 2.5 PFLOP/s).  64 such experts of 7168 channels, for seconds, run at the card's
+// power limit: 2.7 to 2.8 PFLOP/s with the SM clock at 1.5 GHz.
 #include <pthread.h>
 
 #include <atomic>
@@ -711,9 +713,11 @@ static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cud
 
 // Into how many parts a tile's channels are split so that few tiles use the
 // card: at least four stages each, and no more clusters than fit at once (of 152
-// SMs, 15 clusters of eight, 36 of four, 76 of two).  2 experts x 8 rows, gated,
-// 2 x 2048 x 7168, 32 tiles: 22.6 us in one part, 16.2 in two, 13.4 in four; one
-// expert: 22.4 and in eight 12.1.
+// SMs, 15 clusters of eight, 36 of four, 76 of two).  Gated, 8 rows an expert, in
+// one, two, four and eight parts: 2 experts x 2048 columns, 32 tiles, 22.6, 16.1,
+// 13.2 and 32.8 us (four are taken); one expert, 16 tiles, 22.5, 15.6, 12.2 and 21.9
+// (four: the 16 clusters of eight do not fit); one expert x 1024 columns, 8 tiles,
+// two, four, eight: 15.5, 11.7, 11.2 (eight).  All over 7168 channels.
 static int split_parts(long long tiles, int C) {
     const int stages = (C + kBlockK - 1) / kBlockK;
     for (int parts = 8; parts > 1; parts /= 2)
@@ -725,10 +729,12 @@ static int split_parts(long long tiles, int C) {
 template <bool kTransposed, bool kGated>
 static cudaError_t launch_product(const void *a, const void *w, ProductArgs p, cudaStream_t stream) {
     // Pairs where an expert has more than a single block's rows on average.  64 experts, 7168 x
-    // 2048, rows each: 128: 202 us in pairs, 160 in single blocks; 160: 205 and 236; 256: 212 and
-    // 231; 320: pairs alone 395, single blocks 320, pairs and tails 352.  256 experts, 262144
-    // rows: pairs and tails 3.56 ms, pairs alone 3.62, single blocks 3.75; 65536 rows, transposed,
-    // 4096 to 7168: 2.24, 2.48 and 2.36 ms.
+    // 2048, rows each: 128: 188 us in pairs, 158 in single blocks; 160: 198 and 207; 256: 207 and
+    // 230; 320: pairs and tails 360, pairs alone 380, single blocks 300.  256 experts of random
+    // counts, in short runs: 262144 rows, pairs and tails 3.30 ms, pairs alone 3.28 to 3.33, single
+    // blocks 3.39 to 3.41; 65536 rows, transposed, 4096 to 7168: 1.95, 2.16 to 2.19 and 1.89 to
+    // 1.95 ms.  The tails start beside the pairs' end and wait for it: their reads may not come
+    // before (see the kernel's wait).
     if (p.rows > (long long)p.E * kRowTile) {
         const cudaError_t e = launch_tiles<2, 256, kTransposed, kGated>(a, w, p, stream);
         if (e != cudaSuccess) return e;

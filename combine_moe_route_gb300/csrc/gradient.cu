@@ -49,7 +49,7 @@ static cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int 
 // third of the kernel's instructions).
 //
 // Bound by HBM: 32768 tokens, top-8, H = 7168 to FP8 rows and logits move 6.2 GB
-// in 936 us (6.62 TB/s, 0.98 of the measured copy rate), to bf16 rows 8.0 GB in
+// in 929 us (6.68 TB/s, 0.99 of the measured copy rate), to bf16 rows 8.0 GB in
 // 1198 us.  Small blocks, many to an SM, keep loads in flight while others
 // divide and store: 256 threads x 3 blocks took 1038 us, 128 x 6 950, 128 x 8
 // 960; 1003 tokens take 31.0 us, and 37.4 us with 6 blocks, whose last wave is
@@ -170,7 +170,7 @@ cudaError_t launch_combine_backward(const void *dout, const void *y, const int32
                                     const int32_t *topk_idx, int T, int K, int H, long long rows, int E, bool fp8,
                                     void *dy, float *dy_scale, float *dtopk_w, float *dlogits, cudaStream_t stream) {
     const size_t smem = dlogits ? (size_t)E * 4 : 0;
-    // as many whole warps as share the row's chunks evenly (H = 7168: 224 threads, 4 chunks each)
+    // as many whole warps as share the row's chunks evenly (H = 7168: 128 threads, 7 chunks each)
     const int nchunk = H / 8, rounds = (nchunk + kGradThreads - 1) / kGradThreads;
     const int threads = ((nchunk + rounds - 1) / rounds + 31) / 32 * 32;
     const __nv_bfloat16 *db = static_cast<const __nv_bfloat16 *>(dout), *yb = static_cast<const __nv_bfloat16 *>(y);

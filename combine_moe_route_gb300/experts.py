@@ -6,7 +6,8 @@ Forward: route -> FP8 dispatch -> gated first product (quantised by its own epil
 product -> combine.  Backward: combine gradient (quantised) -> transposed second product -> gate
 gradient (quantised) -> transposed first product -> dispatch gradient, with the router's gradient
 from the combine's.  The weights are quantised parameters and get no gradient; the quantisations
-pass gradients through unchanged.
+pass gradients through unchanged.  Autograd records neither pass: a tensor that requires a gradient
+gets none through ``expert_layer``, only from ``expert_layer_backward``.
 
 ``python -m combine_moe_route_gb300.experts`` runs one layer both ways on the GPU.
 """

@@ -19,6 +19,8 @@ _API = {
     "combine_partial_send", "combine_partial_recv", "BoundLayer",
     "expert_gemm", "expert_gated_gemm", "expert_gated_backward", "combine_backward", "dispatch_backward",
     "GatedResult", "CombineGrad", "get_expert_error",
+    "quantize_mx4", "dequantize_mx4", "expert_gemm_mx4", "expert_gated_gemm_mx4",
+    "rms_norm", "rms_norm_backward", "rms_norm_workspace_bytes", "NormResult", "NormGrad",
 }
 
 _LAYER = {"expert_layer", "expert_layer_backward", "ExpertWeights", "ExpertForward", "quantize_blocks"}

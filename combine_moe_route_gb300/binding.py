@@ -114,6 +114,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.moe_combine_backward.restype = i32
         lib.moe_dispatch_backward.argtypes = [vp, vp, i32, i32, i32, i64, i32, vp, vp]
         lib.moe_dispatch_backward.restype = i32
+        f32 = ctypes.c_float
+        lib.moe_quantize_mx4.argtypes = [vp, i32, i64, i32, vp, vp, vp]
+        lib.moe_quantize_mx4.restype = i32
+        lib.moe_dequantize_mx4.argtypes = [vp, vp, i64, i32, i32, vp, vp]
+        lib.moe_dequantize_mx4.restype = i32
+        lib.moe_expert_gemm_mx4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+        lib.moe_expert_gemm_mx4.restype = i32
+        lib.moe_expert_gated_gemm_mx4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        lib.moe_expert_gated_gemm_mx4.restype = i32
+        lib.moe_rms_norm.argtypes = [vp, vp, vp, i32, i32, f32, vp, vp, vp, vp, vp]
+        lib.moe_rms_norm.restype = i32
+        lib.moe_rms_norm_workspace_bytes.argtypes = [i32, i32]
+        lib.moe_rms_norm_workspace_bytes.restype = sz
+        lib.moe_rms_norm_backward.argtypes = [vp, vp, vp, vp, i32, i32, f32, vp, vp, vp, sz, vp]
+        lib.moe_rms_norm_backward.restype = i32
         for reader in ("moe_trace_dispatch", "moe_trace_combine"):   # builds with -DMOE_TRACE only
             try:
                 fn = getattr(lib, reader)
@@ -830,6 +845,116 @@ def expert_gated_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w
     return GatedResult(out, out_scale, h)
 
 
+# ---------------------------------------------------------------------------
+# 4-bit rows (e2m1 values, one power-of-two scale per 32 channels) and their products
+# ---------------------------------------------------------------------------
+
+_CODES = tuple(t for t in (torch.uint8, getattr(torch, "float4_e2m1fn_x2", None)) if t is not None)
+_E8M0 = tuple(t for t in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if t is not None)
+
+
+def quantize_mx4(x: torch.Tensor, *, out: torch.Tensor | None = None, out_scale: torch.Tensor | None = None,
+                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """x [..., C] bf16 or fp32 to 4 bits: (codes uint8 [..., C/2], two to a byte, the first in the low
+    half; scales uint8 [..., C/32], 2^(byte - 127)).  A block of 32 with an infinity or a NaN reads back
+    as NaN."""
+    _dev(x, "x", (torch.bfloat16, torch.float32))
+    if x.dim() < 1 or x.shape[-1] % 32 or not x.shape[-1]:
+        raise ValueError("x must be [..., C] with C a multiple of 32")
+    lead, C = tuple(x.shape[:-1]), x.shape[-1]
+    if out is None:
+        out = torch.empty((*lead, C // 2), dtype=torch.uint8, device=x.device)
+    if out_scale is None:
+        out_scale = torch.empty((*lead, C // 32), dtype=torch.uint8, device=x.device)
+    _dev(out, "out", _CODES, (*lead, C // 2))
+    _dev(out_scale, "out_scale", _E8M0, (*lead, C // 32))
+    _on(x, out, out_scale)
+    _enqueue("moe_quantize_mx4", x, stream, x.data_ptr(), _DTYPE_BF16 if x.dtype is torch.bfloat16 else _DTYPE_FP32,
+             x.numel() // C, C, out.data_ptr(), out_scale.data_ptr())
+    return out, out_scale
+
+
+def dequantize_mx4(q: torch.Tensor, scale: torch.Tensor | None, *, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The values of 4-bit rows, exactly: bf16 [..., C] for codes [..., C/2] and scales [..., C/32], or
+    without scales the codes' own values (0 to 6) in e4m3."""
+    _dev(q, "q", _CODES)
+    if q.dim() < 1 or q.shape[-1] % 16 or not q.shape[-1]:
+        raise ValueError("q must be [..., C/2] with C a multiple of 32")
+    lead, C = tuple(q.shape[:-1]), 2 * q.shape[-1]
+    dtype = torch.float8_e4m3fn if scale is None else torch.bfloat16
+    if scale is not None:
+        _dev(scale, "scale", _E8M0, (*lead, C // 32))
+    if out is None:
+        out = torch.empty((*lead, C), dtype=dtype, device=q.device)
+    _dev(out, "out", dtype, (*lead, C))
+    _on(q, scale, out)
+    _enqueue("moe_dequantize_mx4", q, stream, q.data_ptr(), _ptr(scale), q.numel() // (C // 2), C,
+             _DTYPE_FP8 if scale is None else _DTYPE_BF16, out.data_ptr())
+    return out
+
+
+def _mx4_operands(a, a_scale, w, w_scale, expert_offsets):
+    _dev(a, "a", _CODES)
+    _dev(w, "w", _CODES)
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, C/2] and w [E, N, C/2]")
+    rows, C = a.shape[0], 2 * a.shape[1]
+    E, N = w.shape[0], w.shape[1]
+    if 2 * w.shape[2] != C:
+        raise ValueError(f"a has {C} channels, the weight contracts over {2 * w.shape[2]}")
+    _dev(a_scale, "a_scale", _E8M0, (rows, C // 32))
+    _dev(w_scale, "w_scale", _E8M0, (E, N, C // 32))
+    _dev(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    _on(a, a_scale, w, w_scale, expert_offsets)
+    return rows, E, N, C
+
+
+def expert_gemm_mx4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                    expert_offsets: torch.Tensor, *, out_dtype: torch.dtype = torch.bfloat16,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The experts' product over rows grouped by expert, in 4 bits -> [rows, N].
+
+    ``a`` [rows, C/2] codes with ``a_scale`` [rows, C/32], ``w`` [E, N, C/2] with ``w_scale``
+    [E, N, C/32] (``quantize_mx4``'s format); rows [expert_offsets[e], expert_offsets[e+1]) meet
+    ``w[e]``."""
+    rows, E, N, C = _mx4_operands(a, a_scale, w, w_scale, expert_offsets)
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
+    _dev(out, "out", out_dtype, (rows, N))
+    _on(a, out)
+    _enqueue("moe_expert_gemm_mx4", a, stream, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+             expert_offsets.data_ptr(), E, N, C, rows, _DTYPE_FP32 if out_dtype is torch.float32 else _DTYPE_BF16,
+             out.data_ptr())
+    return out
+
+
+def expert_gated_gemm_mx4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                          expert_offsets: torch.Tensor, *, out: torch.Tensor | None = None,
+                          out_scale: torch.Tensor | None = None, stream=None) -> GatedResult:
+    """The gated first product in 4 bits: quantize_mx4(silu(a wg^T) * (a wu^T)) for ``w`` =
+    [E, 2I, C/2], the gate's I rows first; the result has codes [rows, I/2] and scales [rows, I/32].
+    A serving form: it keeps nothing for a gradient."""
+    rows, E, N, C = _mx4_operands(a, a_scale, w, w_scale, expert_offsets)
+    if N % 64:
+        raise ValueError("w must be [E, 2*I, C/2] with I a multiple of 32")
+    inner, dev = N // 2, a.device
+    if out is None:
+        out = torch.empty((rows, inner // 2), dtype=torch.uint8, device=dev)
+    if out_scale is None:
+        out_scale = torch.empty((rows, inner // 32), dtype=torch.uint8, device=dev)
+    _dev(out, "out", _CODES, (rows, inner // 2))
+    _dev(out_scale, "out_scale", _E8M0, (rows, inner // 32))
+    _on(a, out, out_scale)
+    _enqueue("moe_expert_gated_gemm_mx4", a, stream, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
+             w_scale.data_ptr(), expert_offsets.data_ptr(), E, inner, C, rows, out.data_ptr(), out_scale.data_ptr())
+    return GatedResult(out, out_scale, None)
+
+
 def get_expert_error(device=None, stream=None) -> tuple[int, int]:
     """Synchronise the stream, read and clear the device's error word of the expert products, which
     all of its streams share: (status, raw bits)."""
@@ -951,3 +1076,103 @@ def dispatch_backward(drows: torch.Tensor, tok2row: torch.Tensor, K: int, *,
     _enqueue("moe_dispatch_backward", drows, stream, drows.data_ptr(), tok2row.data_ptr(), T, K, H, rows,
              _DTYPE_FP32 if out_dtype is torch.float32 else _DTYPE_BF16, out.data_ptr())
     return out
+
+
+# ---------------------------------------------------------------------------
+# the norm in front of a layer
+# ---------------------------------------------------------------------------
+
+@dataclass
+class NormResult:
+    y: torch.Tensor             # [T, H] bf16
+    h: torch.Tensor             # [T, H] bf16: x + residual (x itself without one)
+    q: torch.Tensor | None      # [T, H] e4m3 (fp8 only)
+    scale: torch.Tensor | None  # [T, H/128] fp32 (fp8 only)
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | None = None, eps: float = 1e-6,
+             fp8: bool = False, out: torch.Tensor | None = None, out_h: torch.Tensor | None = None,
+             out_q: torch.Tensor | None = None, out_scale: torch.Tensor | None = None, stream=None) -> NormResult:
+    """y = s / sqrt(mean(s^2) + eps) * weight for s = x + residual, x [T, H] bf16 and weight [H] bf16;
+    ``h`` of the result is s in bf16.  ``fp8`` also quantises y per 128 channels, by the dispatch's rule.
+    ``out`` and ``out_h`` may be ``x`` or ``residual``."""
+    _dev(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    _dev(weight, "weight", torch.bfloat16, (H,))
+    if not eps >= 0.0:
+        raise ValueError("eps must not be negative")
+    if fp8 and H % 128:
+        raise ValueError("fp8 needs H a multiple of 128")
+    dev = x.device
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _dev(out, "out", torch.bfloat16, (T, H))
+    if residual is not None:
+        _dev(residual, "residual", torch.bfloat16, (T, H))
+        if out_h is None:
+            out_h = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        _dev(out_h, "out_h", torch.bfloat16, (T, H))
+        if out_h.data_ptr() == out.data_ptr() and T:
+            raise ValueError("out and out_h must be two buffers")
+    else:
+        out_h = None
+    if fp8:
+        if out_q is None:
+            out_q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
+        if out_scale is None:
+            out_scale = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
+        _dev(out_q, "out_q", _E4M3, (T, H))
+        _dev(out_scale, "out_scale", torch.float32, (T, H // 128))
+    else:
+        out_q = out_scale = None
+    _on(x, weight, residual, out, out_h, out_q, out_scale)
+    _enqueue("moe_rms_norm", x, stream, x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, eps, out.data_ptr(),
+             _ptr(out_h), _ptr(out_q), _ptr(out_scale))
+    return NormResult(out, x if residual is None else out_h, out_q, out_scale)
+
+
+@dataclass
+class NormGrad:
+    dx: torch.Tensor            # [T, H] bf16: gradient of x, and of the residual
+    dweight: torch.Tensor       # [H] fp32
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, *, dh: torch.Tensor | None = None,
+                      eps: float = 1e-6, out: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> NormGrad:
+    """Gradient of ``rms_norm`` from the ``h`` that it returned: dx = r (g - n mean(g n)) + dh for
+    r = 1 / sqrt(mean(h^2) + eps), n = h r, g = dy * weight (``dh``: the gradient that reaches h past the
+    norm), and dweight = sum of dy * n over the rows.  ``out`` may be ``dy``, ``h`` or ``dh``.
+    ``workspace``: uint8, at least ``rms_norm_workspace_bytes(T, H)``, this call's alone while it runs."""
+    _dev(h, "h", torch.bfloat16)
+    if h.dim() != 2:
+        raise ValueError("h must be [T, H]")
+    T, H = h.shape
+    _dev(dy, "dy", torch.bfloat16, (T, H))
+    _dev(weight, "weight", torch.bfloat16, (H,))
+    if dh is not None:
+        _dev(dh, "dh", torch.bfloat16, (T, H))
+    if not eps >= 0.0:
+        raise ValueError("eps must not be negative")
+    dev = h.device
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if dweight is None:
+        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    _dev(out, "out", torch.bfloat16, (T, H))
+    _dev(dweight, "dweight", torch.float32, (H,))
+    if workspace is None:
+        workspace = torch.empty(max(rms_norm_workspace_bytes(T, H), 16), dtype=torch.uint8, device=dev)
+        if stream is not None:   # dropped here, while the stream has yet to use it
+            workspace.record_stream(stream)
+    _dev(workspace, "workspace", torch.uint8)
+    _on(h, dy, weight, dh, out, dweight, workspace)
+    _enqueue("moe_rms_norm_backward", h, stream, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _ptr(dh), T, H, eps,
+             out.data_ptr(), dweight.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return NormGrad(out, dweight)
+
+
+def rms_norm_workspace_bytes(T: int, H: int) -> int:
+    return int(load_library().moe_rms_norm_workspace_bytes(T, H))

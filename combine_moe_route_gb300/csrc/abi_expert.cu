@@ -1,5 +1,5 @@
-// abi_expert.cu -- the extern "C" entry points of the expert products and the
-// gradients (declared and documented in include/moe_route.h): host-side
+// abi_expert.cu -- the extern "C" entry points of the expert products, the 4-bit
+// rows, the norm and the gradients (declared and documented in include/moe_route.h): host-side
 // argument validation and the kernel launches.  As in abi.cu, nothing here
 // allocates or synchronises, and validation runs before the first CUDA call.
 #include <cuda_runtime.h>
@@ -51,6 +51,83 @@ moe_status moe_expert_gated_gemm(const void *a, const float *a_scale, const void
     if (!aligned16(a) || !aligned16(w) || !aligned16(q) || !aligned16(h)) return MOE_ERR_UNSUPPORTED;
     return cuda_status(moe::launch_expert_gated_gemm(a, a_scale, w, w_scale, expert_offsets, E, I, C, rows, q, q_scale,
                                                      h, (cudaStream_t)stream));
+}
+
+moe_status moe_quantize_mx4(const void *x, moe_dtype x_dtype, int64_t rows, int C, void *q, void *scale,
+                            moe_stream_t stream) {
+    if (rows < 0 || C < 32 || C % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (x_dtype != MOE_DTYPE_BF16 && x_dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
+    if (rows > moe::kMx4Most / (C / 32)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scale) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q)) return MOE_ERR_UNSUPPORTED;
+    return cuda_status(moe::launch_quantize_mx4(x, x_dtype == MOE_DTYPE_FP32, rows * (C / 32), q, scale,
+                                                (cudaStream_t)stream));
+}
+
+moe_status moe_dequantize_mx4(const void *q, const void *scale, int64_t rows, int C, moe_dtype out_dtype, void *out,
+                              moe_stream_t stream) {
+    if (rows < 0 || C < 32 || C % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_FP8_E4M3) return MOE_ERR_INVALID_ARG;
+    if (rows > moe::kMx4Most / (C / 32)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if ((out_dtype == MOE_DTYPE_FP8_E4M3) != (scale == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!q || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
+    return cuda_status(moe::launch_dequantize_mx4(q, scale, rows * (C / 32), out, (cudaStream_t)stream));
+}
+
+moe_status moe_expert_gemm_mx4(const void *a, const void *a_scale, const void *w, const void *w_scale,
+                               const int32_t *expert_offsets, int E, int N, int C, int rows, moe_dtype out_dtype,
+                               void *out, moe_stream_t stream) {
+    if (E < 1 || E > MOE_MAX_EXPERTS || rows < 0) return MOE_ERR_INVALID_ARG;
+    if (!expert_dim_ok(N, 16) || !expert_dim_ok(C, 32)) return MOE_ERR_INVALID_ARG;
+    if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!a || !a_scale || !w || !w_scale || !expert_offsets || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(w) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
+    return cuda_status(moe::launch_expert_gemm_mx4(a, a_scale, w, w_scale, expert_offsets, E, N, C, rows,
+                                                   out_dtype == MOE_DTYPE_FP32, out, (cudaStream_t)stream));
+}
+
+moe_status moe_expert_gated_gemm_mx4(const void *a, const void *a_scale, const void *w, const void *w_scale,
+                                     const int32_t *expert_offsets, int E, int I, int C, int rows, void *q,
+                                     void *q_scale, moe_stream_t stream) {
+    if (E < 1 || E > MOE_MAX_EXPERTS || rows < 0) return MOE_ERR_INVALID_ARG;
+    if (I < 32 || I > MOE_MAX_EXPERT_DIM / 2 || I % 32 != 0 || !expert_dim_ok(C, 32)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!a || !a_scale || !w || !w_scale || !expert_offsets || !q || !q_scale) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(w) || !aligned16(q)) return MOE_ERR_UNSUPPORTED;
+    return cuda_status(moe::launch_expert_gated_gemm_mx4(a, a_scale, w, w_scale, expert_offsets, E, I, C, rows, q,
+                                                         q_scale, (cudaStream_t)stream));
+}
+
+moe_status moe_rms_norm(const void *x, const void *residual, const void *weight, int T, int H, float eps, void *y,
+                        void *h, void *q, float *q_scale, moe_stream_t stream) {
+    if (T < 0 || !hidden_ok(H) || !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (q && H % 128 != 0) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!x || !weight || !y || (residual != nullptr) != (h != nullptr) || (q && !q_scale)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(y) || !aligned16(h) || !aligned16(q))
+        return MOE_ERR_UNSUPPORTED;
+    return cuda_status(moe::launch_rms_norm(x, residual, weight, T, H, eps, y, h, q, q_scale, (cudaStream_t)stream));
+}
+
+size_t moe_rms_norm_workspace_bytes(int T, int H) {
+    return T > 0 && hidden_ok(H) ? moe::norm_workspace_bytes(T, H) : 0;
+}
+
+moe_status moe_rms_norm_backward(const void *dy, const void *h, const void *weight, const void *dh, int T, int H,
+                                 float eps, void *dx, float *dweight, void *workspace, size_t workspace_bytes,
+                                 moe_stream_t stream) {
+    if (T < 0 || !hidden_ok(H) || !(eps >= 0.0f) || !dweight) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!dy || !h || !weight || !dx)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!workspace || workspace_bytes < moe::norm_workspace_bytes(T, H))) return MOE_ERR_WORKSPACE;
+    if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(dh) || !aligned16(dx) ||
+        !aligned16(workspace))
+        return MOE_ERR_UNSUPPORTED;
+    return cuda_status(moe::launch_rms_norm_backward(dy, h, weight, dh, T, H, eps, dx, dweight, workspace,
+                                                     (cudaStream_t)stream));
 }
 
 moe_status moe_get_expert_error(int32_t *host_code, moe_stream_t stream) {

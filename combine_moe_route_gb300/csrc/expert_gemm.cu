@@ -56,23 +56,17 @@
 #include <atomic>
 
 #include "launch.h"
-#include "numeric.cuh"
-#include "tcgen05.cuh"
+#include "product.cuh"
 
 namespace moe {
 
-constexpr int kProductThreads = 384;
 // Registers of a thread of the loading and issuing warpgroup and of the two
 // others, out of the 168 that a block of 384 threads starts with:
 // 40 + 2 * 232 = 3 * 168.
 constexpr int kIssueRegisters = 40, kSumRegisters = 232;
-constexpr int kRowTile = 128;     // rows of a tile: the M of one product
-constexpr int kFewRows = 32;      // rows of the small load of A
 constexpr int kBlockK = 128;      // channels per stage: one scale block, 128 bytes
 constexpr int kStageA = kRowTile * kBlockK;
-constexpr int kStagingWarp = 32 * 64;       // output staging of a warp: 32 rows x 64 bytes
 constexpr int kScaleSlots = 4;             // of the ring of scales
-constexpr int kTmemColumns = 512;
 
 // Set when a bounded wait of a product kernel ran out (never in a sound run), and
 // what the last read took out of it.
@@ -113,11 +107,6 @@ constexpr int weight_box() {
     return (kTransposed || kGated) ? 128 : kBN / kCtas;
 }
 
-// Bytes that a row tile's load of A brings.
-__device__ __forceinline__ uint32_t row_load_bytes(int valid) {
-    return valid > kFewRows ? kRowTile * kBlockK : valid > 0 ? kFewRows * kBlockK : 0;
-}
-
 template <int kCtas, int kBN>
 struct ProductShared {
     uint64_t full[ProductLayout<kCtas, kBN>::kStages], empty[ProductLayout<kCtas, kBN>::kStages];
@@ -133,29 +122,10 @@ struct ProductShared {
     float amax[2][2][kRowTile];            // gated: by tile parity, each warpgroup's maximum of a row's block
 };
 
-// Position in a ring of n slots and the parity of its current pass.
-struct Ring {
-    int slot = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void advance(int n) {
-        if (++slot == n) {
-            slot = 0;
-            parity ^= 1u;
-        }
-    }
-};
-
 struct Tile {
     int e, row0, valid, n;   // expert, this block's first row and rows, column tile
     int pair_valid;          // rows of the blocks together
 };
-
-// Expert e's first row and number of rows, inside [0, rows] whatever the offsets hold.
-__device__ __forceinline__ int2 expert_rows(const ProductArgs &p, int e) {
-    const int lo = min(max(ld_chained(p.expert_offsets + e), 0), p.rows);
-    const int hi = min(max(ld_chained(p.expert_offsets + e + 1), 0), p.rows);
-    return make_int2(lo, max(hi - lo, 0));
-}
 
 // Row tiles of an expert with n rows.  Pairs take its whole 256 rows and a rest
 // of more than 128; a rest of up to 128 rows, half of a pair's tile, is a tile
@@ -180,47 +150,6 @@ __device__ __forceinline__ Tile tile_at(const Shared &s, const ProductArgs &p, l
     const int m = kCtas == 1 && p.tails ? r.y / (2 * kRowTile) * 2 : i % mt * kCtas;   // in units of 128 rows
     const int valid = min(r.y - m * kRowTile, kCtas * kRowTile);
     return {e, r.x + (m + rank) * kRowTile, max(min(valid - rank * kRowTile, kRowTile), 0), i / mt, valid};
-}
-
-// 64 bytes of each of a warp's 32 rows (a lane holds its row's) to global
-// memory, four lanes per row, through the warp's staging, which is swizzled
-// against bank conflicts.  (Each lane writing its own row took three times as
-// long: 32 lines a store.)  `dst` is the address in the warp's row 0, rows lie
-// `pitch` bytes apart.  `keep`: which rows to write, a bit each (kMask) or the first
-// so many (a mask's bits cost a product's tiles 2 %); bytes at or past `limit`
-// are not written.
-template <bool kMask>
-__device__ __forceinline__ void store_rows64(const uint4 (&v)[4], uint32_t stage, unsigned char *dst, size_t pitch,
-                                             uint32_t keep, int limit, int lane) {
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) st_shared_v4(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16), v[c]);
-    __syncwarp();
-    const int c = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2);
-        const uint4 x = ld_shared_v4(stage + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
-        const bool kept = kMask ? (keep >> r & 1u) != 0 : r < (int)keep;
-        if (kept && c * 16 < limit) st_v4(dst + (size_t)r * pitch + c * 16, x);
-    }
-}
-
-// 64 fp32 values of a row, as bf16.
-template <bool kMask>
-__device__ __forceinline__ void store_bf16x64(const float2 *acc, uint32_t stage, unsigned char *dst, size_t pitch,
-                                              uint32_t keep, int limit, int lane) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        uint4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 *a = acc + c * 16 + i * 4;
-            v[i] = make_uint4(bf16_pair(a[0].x, a[0].y), bf16_pair(a[1].x, a[1].y), bf16_pair(a[2].x, a[2].y),
-                              bf16_pair(a[3].x, a[3].y));
-        }
-        store_rows64<kMask>(v, stage, dst + c * 64, pitch, keep, limit - c * 64, lane);
-    }
 }
 
 // kSplit: the blocks of a cluster share one tile, each taking a run of its
@@ -637,38 +566,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
 // ------------------------------------------------------------------- host
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiled encode_tiled() {
-    static std::atomic<EncodeTiled> fn{nullptr};
-    EncodeTiled f = fn.load(std::memory_order_acquire);
-    if (!f) {
-        void *sym = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess || found != cudaDriverEntryPointSuccess)
-            return nullptr;
-        f = reinterpret_cast<EncodeTiled>(sym);
-        fn.store(f, std::memory_order_release);
-    }
-    return f;
-}
-
-// Byte tensor of up to 3 dimensions (x innermost, dense), boxes of 128 x ny (x 1), 128-byte swizzle.
-static bool encode_bytes(CUtensorMap *map, const void *base, uint64_t x, uint64_t y, uint64_t z, int ny) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
-    const int rank = z ? 3 : 2;
-    const cuuint64_t dims[3] = {x, y, z};
-    const cuuint64_t strides[2] = {x, x * y};
-    const cuuint32_t box[3] = {128, (cuuint32_t)ny, 1}, elem[3] = {1, 1, 1};
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), dims, strides, box, elem,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int kCtas, int kBN, bool kTransposed, bool kGated, bool kSplit = false>
 static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cudaStream_t stream) {
     CUtensorMap map_a, map_few, map_w;
@@ -678,16 +575,9 @@ static cudaError_t launch_tiles(const void *a, const void *w, ProductArgs p, cud
         return cudaErrorInvalidValue;
     auto kernel = expert_product_kernel<kCtas, kBN, kTransposed, kGated, kSplit>;
     constexpr int smem = ProductLayout<kCtas, kBN>::kBytes;
-    static std::atomic<uint64_t> ready{0};   // devices whose limit is raised
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = raise_shared_limit(reinterpret_cast<const void *>(kernel), smem, ready);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit, std::memory_order_release);
-    }
     const int cols = kGated ? kBN / 2 : kBN;
     p.ntiles = ((kGated ? p.N / 2 : p.N) + cols - 1) / cols;
     // no more tiles than this exist; the blocks walk them
@@ -772,6 +662,10 @@ cudaError_t launch_expert_gated_gemm(const void *a, const float *a_scale, const 
     p.E = E, p.N = 2 * I, p.C = C, p.rows = (int)rows;
     p.q = static_cast<unsigned char *>(q), p.q_scale = q_scale, p.h = static_cast<__nv_bfloat16 *>(h);
     return launch_product<false, true>(a, w, p, stream);
+}
+
+cudaError_t product_error_word(int32_t **word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_product_error);
 }
 
 // Read and cleared in one step: a product on another stream whose wait runs out

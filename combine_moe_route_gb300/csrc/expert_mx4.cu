@@ -1,0 +1,601 @@
+// expert_mx4.cu -- the experts' products over rows grouped by expert, in 4-bit
+// values with a power-of-two scale per 32 channels of a row and of a weight's row.
+//
+//   p[r, n] = sum_b 2^(ea[r, b] + ew[e, n, b]) * sum_{c in b} a[r, c] * w[e, n, c]
+//
+// The tensor cores apply these scales themselves and add all channels in one fp32
+// accumulator, so a tile of the result is read once, when it is done.
+//
+// A persistent block per SM walks output tiles of 128 rows of one expert x kBN
+// columns (the tiles' order, row loads and the split of a tile's channels over a
+// cluster are those of the e4m3 products).  The warps of a block have fixed jobs:
+//   warp 8       loads the 4-bit tiles of both operands, 256 channels a stage, with
+//                tiled bulk tensor copies into a ring of stages;
+//   warp 9       copies a stage's scales to tensor memory and issues its products
+//                (4 x K = 64);
+//   warps 10, 11 take turns at bringing the scales of two stages from their rows
+//                (16 bytes each) to the order the tensor cores want: 128 rows' words
+//                of four scales, row 32 j + p at byte 16 p + 4 j, so that a lane
+//                holds the words of four rows and writes 16 bytes;
+//   warps 0-7    (two warpgroups) read a finished tile, one row per thread and half
+//                of its columns per warpgroup, and write it, or form silu(g) * u and
+//                quantise it: a block of 32 channels is one thread's.
+// Rows past a tile's own are the next expert's, or hold leftovers; nothing reads
+// them (a row of the result depends on its own row of A and its scales alone).
+#include <atomic>
+
+#include "launch.h"
+#include "mx4.cuh"
+#include "product.cuh"
+
+namespace moe {
+
+// Registers of a thread of the loading, issuing and scaling warpgroup and of the
+// two others, out of the 168 that a block of 384 threads starts with:
+// 104 + 2 * 200 = 3 * 168.
+constexpr int kMx4FeedRegisters = 104, kMx4OutRegisters = 200;
+constexpr int kMx4K = 256;                      // channels per stage: 128 bytes of a row
+constexpr int kMx4StageA = kRowTile * kMx4K / 2;
+constexpr int kScaleTile = 512;                 // bytes: the words of 128 rows, four scales each
+
+struct Mx4Args {
+    const unsigned char *a_scale, *w_scale;
+    const int32_t *expert_offsets;
+    int E, N, C;
+    int rows;
+    int ntiles;         // column tiles
+    int split;          // blocks that share a tile's channels (split launches)
+    int a_width, w_width;   // bytes that a load of scales takes at most: 16, 4 or 1, by their alignment
+    bool tails;         // single blocks: only what the pairs' launch before leaves
+    bool out_f32;
+    void *out;              // plain form: [rows, N]
+    unsigned char *q;       // gated form: [rows, N / 4]
+    unsigned char *q_scale;
+    int32_t *error;
+};
+
+template <int kCtas, int kBN>
+struct Mx4Layout {
+    static constexpr int kWeight = kMx4StageA;                          // a stage's parts
+    static constexpr int kScales = kWeight + kBN / kCtas * kMx4K / 2;
+    static constexpr int kGroups = 1 + kBN / 128;                       // of 128 rows of scales: A's and the weight's
+    static constexpr int kStageBytes = kScales + kGroups * 2 * kScaleTile;
+    // of 227 KB: 4.5 KB for the barriers and the experts' tiles, the output's staging, alignment
+    static constexpr int kStages = (227 * 1024 - 4608 - 8 * kStagingWarp - 1024) / kStageBytes;
+    static constexpr int kStaging = kStages * kStageBytes;
+    static constexpr int kBytes = kStaging + 8 * kStagingWarp + 1024;
+    static constexpr int kAccs = kBN == 128 ? 2 : 1;                    // accumulators in turn
+    static constexpr int kTmemScales = kAccs * kBN;                     // columns from here: 8 per group
+};
+
+template <int kCtas, int kBN>
+struct Mx4Shared {
+    uint64_t full[Mx4Layout<kCtas, kBN>::kStages], empty[Mx4Layout<kCtas, kBN>::kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t warp_tiles[kProductThreads / 32];
+    int32_t tiles[MOE_MAX_EXPERTS + 1];    // row tiles before expert e
+};
+
+// Row tiles of an expert with n rows: pairs take its whole 256 rows and a rest of
+// more than 128, a rest of up to 128 is a tile of the single blocks' launch that
+// follows (`tails`).  Without pairs single blocks take every 128 rows.
+template <int kCtas>
+__device__ __forceinline__ int mx4_row_tiles(const Mx4Args &p, int n) {
+    constexpr int kPair = 2 * kRowTile;
+    if (kCtas == 2) return n / kPair + (n % kPair > kRowTile);
+    if (p.tails) return n % kPair > 0 && n % kPair <= kRowTile;
+    return (n + kRowTile - 1) / kRowTile;
+}
+
+struct Mx4Tile {
+    int e, row0, valid, n;   // expert, this block's first row and rows, column tile
+    int pair_valid;          // rows of the blocks together
+};
+
+// Tile t: experts in order; within an expert the row tiles of one column tile
+// come first, so that blocks working at the same time share the weight.
+template <int kCtas, class Shared>
+__device__ __forceinline__ Mx4Tile mx4_tile(const Shared &s, const Mx4Args &p, long long t, int rank) {
+    const int e = upper_bound_minus_one(s.tiles, p.E, (int)(t / p.ntiles));
+    const int mt = s.tiles[e + 1] - s.tiles[e];
+    const int i = (int)(t - (long long)s.tiles[e] * p.ntiles);
+    const int2 r = expert_rows(p, e);
+    const int m = kCtas == 1 && p.tails ? r.y / (2 * kRowTile) * 2 : i % mt * kCtas;   // in units of 128 rows
+    const int valid = min(r.y - m * kRowTile, kCtas * kRowTile);
+    return {e, r.x + (m + rank) * kRowTile, max(min(valid - rank * kRowTile, kRowTile), 0), i / mt, valid};
+}
+
+// 16 scales of a row, those past its end as 0 (their channels are 0 too).
+__device__ __forceinline__ uint4 load_scales(const unsigned char *p, int left, int width) {
+    if (width == 16) return left > 0 ? ld_cached_v4(p) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (width == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * i < left) w[i] = (uint32_t)ld_chained(reinterpret_cast<const int32_t *>(p) + i);
+    } else {
+        for (int i = 0; i < min(left, 16); ++i) {
+            const uint32_t b = ld_chained(p + i) << (8 * (i & 3));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i >> 2 == j) w[j] |= b;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+template <int kCtas, int kBN, bool kGated, bool kSplit>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    expert_mx4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_few,
+                      const __grid_constant__ CUtensorMap map_w, const Mx4Args p) {
+    using Layout = Mx4Layout<kCtas, kBN>;
+    constexpr int kTileColumns = kGated ? kBN / 2 : kBN;   // of the result
+    extern __shared__ unsigned char s_raw[];
+    __shared__ Mx4Shared<kCtas, kBN> s;
+    unsigned char *tiles = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);   // swizzled tiles: 1024-byte aligned
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const bool issue = lane == 0;
+    const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
+    const int nkb = (p.C + kMx4K - 1) / kMx4K;
+    const int parts = kSplit ? p.split : 1, part = kSplit ? (int)cluster_rank() : 0;
+    // this block's channels, from an even stage on: a load of scales is two stages' and stays aligned
+    const int kb_first = kSplit ? (nkb + 1) / 2 * part / parts * 2 : 0;
+    const int nk = kSplit ? min((nkb + 1) / 2 * (part + 1) / parts * 2, nkb) - kb_first : nkb;
+
+    // prologue: barriers, tensor memory, and the experts' row tiles
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Layout::kStages; ++i) {
+            mbar_init(&s.full[i], 1 + kCtas);   // the loads' bytes, each block's scales
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], 8 * kCtas);
+        }
+        mbar_init(&s.drain, 1);
+        fence_mbarrier_init();
+        prefetch_tensor_map(&map_a);
+        prefetch_tensor_map(&map_few);
+        prefetch_tensor_map(&map_w);
+    }
+    if (warp == 9) tmem_alloc<kCtas, kTmemColumns>(&s.tmem);
+    // Up to here nothing is read: this block may have started while the kernel before ran out, and
+    // lets the kernel after do the same.  Only this wait makes what earlier kernels wrote visible.
+    pdl_launch_dependents();
+    pdl_wait();
+    {
+        constexpr int kPer = (MOE_MAX_EXPERTS + kProductThreads - 1) / kProductThreads;
+        int mine = 0, mt[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            mt[i] = 0;
+            if (e < p.E) mt[i] = mx4_row_tiles<kCtas>(p, expert_rows(p, e).y);
+            mine += mt[i];
+        }
+        int sum = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += v;
+        }
+        if (lane == 31) s.warp_tiles[warp] = sum;
+        __syncthreads();
+        // 64 bits and a cap: offsets that overlap may not make the prefix wrap
+        long long before = sum - mine;
+        for (int w = 0; w < warp; ++w) before += s.warp_tiles[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            if (e < p.E) s.tiles[e] = (int)min(before, 1ll << 30);
+            before += mt[i];
+            if (e == p.E - 1) s.tiles[p.E] = (int)min(before, 1ll << 30);
+        }
+    }
+    tcgen05_fence_before();
+    if (kCtas == 2) cluster_barrier();   // the pair's barriers are ready
+    else __syncthreads();
+    tcgen05_fence_after();
+    const long long total = (long long)s.tiles[p.E] * p.ntiles;
+    const long long stride = kSplit ? total : gridDim.x / kCtas;
+    const uint32_t tmem = s.tmem;
+
+    // Every wait below has a limit and runs out on its own if its partner has left; a role whose
+    // wait ran out leaves its loop.
+    const auto at = [](const uint64_t *bar) { return smem_u32(bar); };
+    const uint32_t tiles_at = smem_u32(tiles);
+    bool go = true;
+    if (warp >= 8) {
+        registers_decrease<kMx4FeedRegisters>();
+        if (warp == 8) {
+            // ---------------------------------------------------- loads
+            Ring r;
+            long long issued = 0;
+            for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += stride) {
+                const Mx4Tile tile = mx4_tile<kCtas>(s, p, t, rank);
+                // a pair splits the columns: each block brings half of them; the gate's and the
+                // up projection's lie apart
+                constexpr int kBox = kGated ? 128 : kBN / kCtas, kBoxBytes = kBox * kMx4K / 2;
+                constexpr int kBoxes = kBN / kCtas / kBox;
+                const int first = tile.n * kTileColumns + rank * (kGated ? p.N / 2 : kBox);
+                const CUtensorMap *rows = tile.valid > kFewRows ? &map_a : &map_few;
+                const uint32_t bytes =
+                    kCtas * kBoxes * kBoxBytes +
+                    (kCtas == 2 ? row_load_bytes(min(tile.pair_valid, kRowTile)) +
+                                      row_load_bytes(tile.pair_valid - kRowTile)
+                                : row_load_bytes(tile.valid));
+                for (int kb = kb_first; kb < kb_first + nk; ++kb) {
+                    go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.empty[r.slot]), r.parity ^ 1u));
+                    if (!go) break;
+                    const uint32_t a = tiles_at + r.slot * Layout::kStageBytes, w = a + Layout::kWeight;
+                    const uint32_t bar = at(&s.full[r.slot]);
+#ifdef MOE_TEST_WITHHOLD_PRODUCT_STAGE
+                    // Test builds only: the loads of this stage never happen, so the waits run out.
+                    const bool load = issue && issued != MOE_TEST_WITHHOLD_PRODUCT_STAGE;
+#else
+                    const bool load = issue;
+#endif
+                    mbar_expect(bar, bytes, load && rank == 0);
+                    tensor_load_2d<kCtas>(a, rows, kb * (kMx4K / 2), tile.row0, bar, load && tile.valid > 0);
+#pragma unroll
+                    for (int i = 0; i < kBoxes; ++i)
+                        tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, kb * (kMx4K / 2),
+                                              first + i * (kGated ? p.N / 2 : kBox), tile.e, bar, load);
+                    r.advance(Layout::kStages);
+                    ++issued;
+                }
+            }
+            // nothing in flight when the block ends: the products have read every stage, or (after
+            // a wait ran out) at least its loads have landed
+            const int last = (int)(issued < Layout::kStages ? issued : Layout::kStages);
+            for (int i = 0; i < last; ++i) {
+                r.slot = (r.slot == 0 ? Layout::kStages : r.slot) - 1;
+                if (r.slot == Layout::kStages - 1) r.parity ^= 1u;
+                go = go && __all_sync(0xffffffffu, mbar_wait_polls(at(&s.empty[r.slot]), r.parity));
+                if (!go && rank == 0)   // a pair's barrier counts both blocks' loads
+                    mbar_wait_polls(at(&s.full[r.slot]), r.parity);
+            }
+        } else if (warp == 9) {
+            // ------------------------------------------------- products
+            if (rank == 0) {
+                constexpr uint32_t instruction = mx4_instruction(kCtas * kRowTile, kBN);
+                const uint64_t a0 = smem_descriptor(tiles_at, 16, 1024);
+                const uint64_t w0 = smem_descriptor(tiles_at + Layout::kWeight, 16, 1024);
+                const uint64_t s0 = scales_descriptor(tiles_at + Layout::kScales);
+                const uint32_t scales = tmem + Layout::kTmemScales;
+                Ring r, acc;
+                for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += stride) {
+                    go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.acc_empty[acc.slot]), acc.parity ^ 1u));
+                    if (!go) break;
+                    tcgen05_fence_after();
+                    const uint32_t d = tmem + acc.slot * kBN;
+                    for (int kb = 0; kb < nk; ++kb) {
+                        const bool full = mbar_wait_polls(at(&s.full[r.slot]), r.parity);
+                        tcgen05_fence_after();
+                        const uint64_t step = (uint32_t)r.slot * (Layout::kStageBytes >> 4);
+                        // group g's scales of the stage's first and second 128 channels: columns
+                        // 4 g on of the first or second run of kGroups * 4
+#pragma unroll
+                        for (int j = 0; j < 2 * Layout::kGroups; ++j)
+                            tmem_copy_scales<kCtas>(scales + j * 4, s0 + step + j * (kScaleTile >> 4), issue);
+#pragma unroll
+                        for (int k = 0; k < kMx4K / 64; ++k) {
+                            const uint32_t from = scales + (k >> 1) * Layout::kGroups * 4;
+                            mma_mx4<kCtas>(d, a0 + step + k * 2, w0 + step + k * 2, instruction | mx4_scales((k & 1) * 2),
+                                           from, from + 4, kb > 0 || k > 0, issue);
+                        }
+                        mma_commit<kCtas>(at(&s.empty[r.slot]), issue);
+                        r.advance(Layout::kStages);
+                        go = __all_sync(0xffffffffu, full);
+                        if (!go) break;
+                    }
+                    mma_commit<kCtas>(at(&s.acc_full[acc.slot]), issue);
+                    acc.advance(Layout::kAccs);
+                }
+                if (!go) {   // leave no product running
+                    mma_commit<kCtas>(at(&s.drain), issue);
+                    mbar_wait_polls(at(&s.drain), 0);
+                }
+            }
+        } else {
+            // --------------------------------------------------- scales
+            // Two stages at a time, this warp every other time; the loads of its next time are
+            // in flight while it waits for the stages of this one to be free.
+            const int turn = warp - 10;
+            const int a_bytes = p.C / kMx4Block;
+            const uint32_t full0 = kCtas == 2 ? first_block_address(at(&s.full[0])) : 0;
+            Ring r;
+            long long t = blockIdx.x / (kCtas * parts);
+            int kb = 0;
+            Mx4Tile tile = {};
+            if (t < total) tile = mx4_tile<kCtas>(s, p, t, rank);
+            const auto step = [&] {   // to the next two stages
+                for (int i = 0; i < 2 && kb < nk; ++i, ++kb) r.advance(Layout::kStages);
+                if (kb < nk) return;
+                kb = 0;
+                t += stride;
+                if (t < total) tile = mx4_tile<kCtas>(s, p, t, rank);
+            };
+            uint4 v[Layout::kGroups][4];
+            const auto load = [&] {
+                const int byte = (kb_first + kb) * (kMx4K / kMx4Block);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int row = q * 32 + lane;
+                    v[0][q] = row < tile.valid
+                                  ? load_scales(p.a_scale + (size_t)(tile.row0 + row) * a_bytes + byte, a_bytes - byte,
+                                                p.a_width)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int g = 1; g < Layout::kGroups; ++g) {
+                        const int column = tile.n * kTileColumns + row + (g - 1) * (kGated ? p.N / 2 : 128);
+                        v[g][q] = load_scales(
+                            p.w_scale + ((size_t)tile.e * p.N + min(column, p.N - 1)) * a_bytes + byte, a_bytes - byte,
+                            p.w_width);
+                    }
+                }
+            };
+            if (turn == 1 && t < total) step();
+            if (t < total) load();
+            while (go && t < total) {
+                const int count = min(2, nk - kb);
+                Ring c = r;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i == count) break;
+                    go = go && __all_sync(0xffffffffu, mbar_wait_polls(at(&s.empty[c.slot]), c.parity ^ 1u));
+                    if (!go) break;
+                    const uint32_t to = tiles_at + c.slot * Layout::kStageBytes + Layout::kScales + lane * 16;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int g = 0; g < Layout::kGroups; ++g)
+                            st_shared_v4(to + (j * Layout::kGroups + g) * kScaleTile,
+                                         make_uint4(word_of(v[g][0], i * 2 + j), word_of(v[g][1], i * 2 + j),
+                                                    word_of(v[g][2], i * 2 + j), word_of(v[g][3], i * 2 + j)));
+                    fence_proxy_async_smem();   // the copies to tensor memory read them
+                    __syncwarp();
+                    if (kCtas == 2) mbar_release_cluster(full0 + c.slot * 8, issue);
+                    else mbar_arrive(at(&s.full[c.slot]), issue);
+                    c.advance(Layout::kStages);
+                }
+                step();
+                if (t < total) step();
+                if (t < total) load();
+            }
+        }
+        if (kSplit) {   // the sums' exchange below
+            cluster_barrier();
+            cluster_barrier();
+        }
+    } else {
+        // ------------------------------------------------ the output
+        registers_increase<kMx4OutRegisters>();
+        // a warpgroup takes half of the columns, in groups of 64: of the gate's and of the up
+        // projection's (h = 0, 1), or side by side
+        constexpr int kHalves = kBN / 128;
+        constexpr int kApart = kGated ? 128 : 64;                    // from one group to the next
+        constexpr int kFirst = kGated || kHalves == 1 ? 64 : 128;    // from one warpgroup's first to the other's
+        const int wg = warp >> 2, quarter = warp & 3;
+        const uint32_t stage = tiles_at + Layout::kStaging + warp * kStagingWarp;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + wg * kFirst;
+        const uint32_t first_empty = kCtas == 2 ? first_block_address(at(&s.acc_empty[0])) : 0;   // 8 bytes each
+        Ring acc;
+        for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += stride) {
+            const Mx4Tile tile = mx4_tile<kCtas>(s, p, t, rank);
+            float2 v[kHalves * 32];
+            {
+                uint32_t r[kHalves * 4][16];
+                go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.acc_full[acc.slot]), acc.parity));
+                tcgen05_fence_after();
+#pragma unroll
+                for (int k = 0; k < kHalves * 4; ++k)
+                    tmem_load(lanes + acc.slot * kBN + (k / 4) * kApart + (k & 3) * 16, r[k]);
+#pragma unroll
+                for (int k = 0; k < kHalves * 4; ++k) {
+                    tmem_wait_load(r[k]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[k * 8 + j] = make_float2(__uint_as_float(r[k][2 * j]), __uint_as_float(r[k][2 * j + 1]));
+                }
+                tcgen05_fence_before();   // all read: the accumulator is free
+                if (kCtas == 2) mbar_arrive_cluster(first_empty + acc.slot * 8, issue);
+                else mbar_arrive(at(&s.acc_empty[acc.slot]), issue);
+                acc.advance(Layout::kAccs);
+            }
+            uint32_t keep;   // rows of this warp that are this block's to write: a mask (kSplit) or how many
+            if constexpr (kSplit) {
+                const int row = quarter * 32 + lane, owner = row % parts;
+                const bool valid = go && row < tile.valid;
+                constexpr int kRowBytes = kBN * 4 + 16;   // no bank conflicts between rows
+                // part q's sums of the owner's rows, one after the other
+                const auto room = [&](int q) {
+                    return tiles_at + (q * (kRowTile / parts) + row / parts) * kRowBytes + wg * kBN * 2;
+                };
+                cluster_barrier();   // every block's products are done with its ring
+                if (valid && owner != part) {
+                    const uint32_t to = block_address(room(part), owner);
+#pragma unroll
+                    for (int i = 0; i < kHalves * 16; ++i)
+                        st_cluster_v4(to + i * 16, make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y));
+                }
+                cluster_barrier();
+                if (valid && owner == part) {
+                    for (int q = 0; q < parts; ++q) {   // ascending, after the own: an order that never changes
+                        if (q == part) continue;
+                        const uint32_t from = room(q);
+#pragma unroll
+                        for (int i = 0; i < kHalves * 16; ++i) {
+                            const uint4 x = ld_shared_v4(from + i * 16);
+                            v[2 * i].x += __uint_as_float(x.x);
+                            v[2 * i].y += __uint_as_float(x.y);
+                            v[2 * i + 1].x += __uint_as_float(x.z);
+                            v[2 * i + 1].y += __uint_as_float(x.w);
+                        }
+                    }
+                }
+                keep = __ballot_sync(0xffffffffu, valid && owner == part);
+            } else {
+                keep = (uint32_t)max(min(tile.valid - quarter * 32, 32), 0);
+            }
+            if (!go) break;
+            const int n0 = tile.n * kTileColumns + wg * kFirst;                // first column
+            const size_t warp_row = (size_t)tile.row0 + quarter * 32;
+            if constexpr (kGated) {
+                const int I = p.N / 2;
+                const size_t row = warp_row + lane;
+                if (kSplit ? (keep >> lane & 1u) != 0 : lane < (int)keep) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        if (n0 + b * kMx4Block >= I) break;
+                        float f[kMx4Block];
+                        uint32_t amax = 0;
+#pragma unroll
+                        for (int k = 0; k < kMx4Block / 2; ++k) {
+                            const float2 g = v[b * 16 + k], u = v[32 + b * 16 + k];
+                            f[2 * k] = g.x * sigmoid(g.x) * u.x;
+                            f[2 * k + 1] = g.y * sigmoid(g.y) * u.y;
+                            amax = max(amax, max(magnitude_bits(f[2 * k]), magnitude_bits(f[2 * k + 1])));
+                        }
+                        const uint32_t byte = mx4_scale_byte(amax);
+                        const float inverse = mx4_inverse(byte);
+                        const size_t block = row * (I / kMx4Block) + n0 / kMx4Block + b;
+                        st_v4(p.q + block * 16, make_uint4(pack_e2m1x8(f, inverse), pack_e2m1x8(f + 8, inverse),
+                                                           pack_e2m1x8(f + 16, inverse), pack_e2m1x8(f + 24, inverse)));
+                        p.q_scale[block] = (unsigned char)byte;
+                    }
+                }
+            } else if (keep != 0 && n0 < p.N) {
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    const int n = n0 + h * 64;
+                    if (!p.out_f32) {
+                        store_bf16x64<kSplit>(v + h * 32, stage,
+                                              static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 2,
+                                              (size_t)p.N * 2, keep, (p.N - n) * 2, lane);
+                        continue;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 v0 = v[h * 32 + c * 8 + 2 * i], v1 = v[h * 32 + c * 8 + 2 * i + 1];
+                            x[i] = make_uint4(__float_as_uint(v0.x), __float_as_uint(v0.y), __float_as_uint(v1.x),
+                                              __float_as_uint(v1.y));
+                        }
+                        store_rows64<kSplit>(x, stage,
+                                             static_cast<unsigned char *>(p.out) + (warp_row * p.N + n + c * 16) * 4,
+                                             (size_t)p.N * 4, keep, (p.N - n) * 4 - c * 64, lane);
+                    }
+                }
+            }
+        }
+        if (kSplit && blockIdx.x / parts >= total) {   // no tile: the exchange is the cluster's all the same
+            cluster_barrier();
+            cluster_barrier();
+        }
+    }
+    if (!go && issue) atomicOr(p.error, MOE_DEVERR_COPY_TIMEOUT);
+    __syncwarp();
+    tcgen05_fence_before();
+    if (kCtas == 2) cluster_barrier();   // nothing of the other block's reaches this one any more
+    else __syncthreads();
+    tcgen05_fence_after();
+    if (warp == 9) tmem_free<kCtas, kTmemColumns>(tmem);
+}
+
+// ------------------------------------------------------------------- host
+
+template <int kCtas, int kBN, bool kGated, bool kSplit = false>
+static cudaError_t launch_mx4_tiles(const void *a, const void *w, Mx4Args p, cudaStream_t stream) {
+    CUtensorMap map_a, map_few, map_w;
+    if (!encode_bytes(&map_a, a, p.C / 2, p.rows, 0, kRowTile) || !encode_bytes(&map_few, a, p.C / 2, p.rows, 0, kFewRows) ||
+        !encode_bytes(&map_w, w, p.C / 2, p.N, p.E, kGated ? 128 : kBN / kCtas))
+        return cudaErrorInvalidValue;
+    auto kernel = expert_mx4_kernel<kCtas, kBN, kGated, kSplit>;
+    constexpr int smem = Mx4Layout<kCtas, kBN>::kBytes;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = raise_shared_limit(reinterpret_cast<const void *>(kernel), smem, ready);
+    if (e != cudaSuccess) return e;
+    const int cols = kGated ? kBN / 2 : kBN;
+    p.ntiles = ((kGated ? p.N / 2 : p.N) + cols - 1) / cols;
+    // no more tiles than this exist; the blocks walk them
+    const long long most = ((p.tails ? 0 : (long long)p.rows / (kCtas * kRowTile)) + (p.rows < p.E ? p.rows : p.E)) *
+                           p.ntiles;
+    const int groups = device_sm_count() / kCtas;
+    cudaLaunchConfig_t cfg = {};
+    const int parts = kSplit ? p.split : 1;
+    cfg.gridDim = dim3((unsigned)(kSplit ? most * parts : kCtas * (most < groups ? (most > 0 ? most : 1) : groups)));
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSplit ? parts : kCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_few, map_w, p);
+}
+
+// Into how many parts a tile's channels are split so that few tiles use the card:
+// at least four stages each, and no more clusters than fit at once.
+static int mx4_split_parts(long long tiles, int C) {
+    const int stages = (C + kMx4K - 1) / kMx4K;
+    for (int parts = 8; parts > 1; parts /= 2)
+        if (tiles * parts <= device_sm_count() * (parts == 8 ? 0.79 : parts == 4 ? 0.95 : 1.0) && stages >= 4 * parts)
+            return parts;
+    return 1;
+}
+
+template <bool kGated>
+static cudaError_t launch_mx4(const void *a, const void *w, Mx4Args p, cudaStream_t stream) {
+    cudaError_t e = product_error_word(&p.error);
+    if (e != cudaSuccess) return e;
+    const auto width = [&](const unsigned char *scale) {
+        const uintptr_t bits = reinterpret_cast<uintptr_t>(scale) | (uintptr_t)(p.C / kMx4Block);
+        return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+    };
+    p.a_width = width(p.a_scale), p.w_width = width(p.w_scale);
+    const long long row_tiles = (long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E);   // at most
+    constexpr int kNarrow = kGated ? 256 : 128;
+    p.split = mx4_split_parts(row_tiles * ((p.N + kNarrow - 1) / kNarrow), p.C);
+    if (p.split > 1) return launch_mx4_tiles<1, kNarrow, kGated, true>(a, w, p, stream);
+    if constexpr (!kGated) {
+        if (row_tiles * ((p.N + 255) / 256) < 4 * device_sm_count()) return launch_mx4_tiles<1, 128, kGated>(a, w, p, stream);
+    }
+    return launch_mx4_tiles<1, 256, kGated>(a, w, p, stream);
+}
+
+cudaError_t launch_expert_gemm_mx4(const void *a, const void *a_scale, const void *w, const void *w_scale,
+                                   const int32_t *expert_offsets, int E, int N, int C, long long rows, bool out_f32,
+                                   void *out, cudaStream_t stream) {
+    Mx4Args p = {};
+    p.a_scale = static_cast<const unsigned char *>(a_scale), p.w_scale = static_cast<const unsigned char *>(w_scale);
+    p.expert_offsets = expert_offsets;
+    p.E = E, p.N = N, p.C = C, p.rows = (int)rows;
+    p.out_f32 = out_f32, p.out = out;
+    return launch_mx4<false>(a, w, p, stream);
+}
+
+cudaError_t launch_expert_gated_gemm_mx4(const void *a, const void *a_scale, const void *w, const void *w_scale,
+                                         const int32_t *expert_offsets, int E, int I, int C, long long rows, void *q,
+                                         void *q_scale, cudaStream_t stream) {
+    Mx4Args p = {};
+    p.a_scale = static_cast<const unsigned char *>(a_scale), p.w_scale = static_cast<const unsigned char *>(w_scale);
+    p.expert_offsets = expert_offsets;
+    p.E = E, p.N = 2 * I, p.C = C, p.rows = (int)rows;
+    p.q = static_cast<unsigned char *>(q), p.q_scale = static_cast<unsigned char *>(q_scale);
+    return launch_mx4<true>(a, w, p, stream);
+}
+
+}  // namespace moe

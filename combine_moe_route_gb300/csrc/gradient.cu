@@ -16,24 +16,6 @@
 
 namespace moe {
 
-// Both kernels here start while the kernel before them in the stream runs out,
-// wait for it before they read, and let the kernel after do the same.
-template <class... Params, class... Args>
-static cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads, size_t smem,
-                                  cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
-}
-
 // --------------------------------------------------------------------------
 // combine backward
 // --------------------------------------------------------------------------

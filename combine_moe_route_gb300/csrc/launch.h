@@ -21,6 +21,24 @@ struct DispatchPlan {
     size_t off_signal, off_status, off_hist, off_scan, total;
 };
 
+// For kernels that start while the kernel before them in the stream runs out, wait
+// for it before they read, and let the kernel after do the same.
+template <class... Params, class... Args>
+inline cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, int threads, size_t smem,
+                                  cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 DispatchPlan plan_dispatch(int E, int R, int ntiles);
 // Whether a dispatch of T tokens with top-K takes the one-kernel path, and the
 // workspace layout the call uses.
@@ -84,5 +102,22 @@ cudaError_t launch_gated_backward(const void *h, const void *dv, long long rows,
 cudaError_t launch_combine_backward(const void *dout, const void *y, const int32_t *tok2row, const float *topk_w,
                                     const int32_t *topk_idx, int T, int K, int H, long long rows, int E, bool fp8,
                                     void *dy, float *dy_scale, float *dtopk_w, float *dlogits, cudaStream_t stream);
+// Where a product's bounded wait that ran out is noted, on the current device.
+cudaError_t product_error_word(int32_t **word);
+cudaError_t launch_expert_gemm_mx4(const void *a, const void *a_scale, const void *w, const void *w_scale,
+                                   const int32_t *expert_offsets, int E, int N, int C, long long rows, bool out_f32,
+                                   void *out, cudaStream_t stream);
+cudaError_t launch_expert_gated_gemm_mx4(const void *a, const void *a_scale, const void *w, const void *w_scale,
+                                         const int32_t *expert_offsets, int E, int I, int C, long long rows, void *q,
+                                         void *q_scale, cudaStream_t stream);
+// Blocks of 32 channels of one call: the 2^31 - 1 blocks of a grid, 256 each.
+constexpr long long kMx4Most = ((1ll << 31) - 1) * 256;
+cudaError_t launch_quantize_mx4(const void *x, bool f32, long long blocks, void *q, void *scale, cudaStream_t stream);
+cudaError_t launch_dequantize_mx4(const void *q, const void *scale, long long blocks, void *out, cudaStream_t stream);
+cudaError_t launch_rms_norm(const void *x, const void *residual, const void *weight, long long T, int H, float eps,
+                            void *y, void *h, void *q, float *q_scale, cudaStream_t stream);
+size_t norm_workspace_bytes(long long T, int H);
+cudaError_t launch_rms_norm_backward(const void *dy, const void *h, const void *weight, const void *dh, long long T,
+                                     int H, float eps, void *dx, float *dweight, void *workspace, cudaStream_t stream);
 
 }  // namespace moe

@@ -111,6 +111,73 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
             : "memory");
 }
 
+// Instruction descriptor: e2m1 x e2m1, both K-major, with power-of-two scales
+// (e8m0), fp32 accumulators, M x N.  Which half of the scales' words an
+// instruction takes is added by mx4_scales(); K = 64.
+__host__ __device__ constexpr uint32_t mx4_instruction(int M, int N) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
+}
+// A scale word holds four scales, of 128 channels along K: `first` = 0 takes the
+// two of its first 64 channels, 2 those of the rest, for both operands.
+__host__ __device__ constexpr uint32_t mx4_scales(int first) {
+    return ((uint32_t)first << 4) | ((uint32_t)first << 29);
+}
+
+// d = a x b (or += with accumulate), 64 channels of 4-bit values with a scale per
+// 32, the scales in tensor memory at scale_a and scale_b.
+template <int kCtas>
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t instruction, uint32_t scale_a,
+                                        uint32_t scale_b, bool accumulate, bool issue) {
+    if (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d),
+            "l"(a), "l"(b), "r"(instruction), "r"(scale_a), "r"(scale_b), "r"((uint32_t)accumulate),
+            "r"((uint32_t)issue)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d),
+            "l"(a), "l"(b), "r"(instruction), "r"(scale_a), "r"(scale_b), "r"((uint32_t)accumulate),
+            "r"((uint32_t)issue)
+            : "memory");
+}
+
+// Descriptor of 512 bytes of scales for the copy below: 32 rows of 16 bytes, one
+// after the other, unswizzled (128 bytes between groups of 8 rows).
+__device__ __forceinline__ uint64_t scales_descriptor(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+
+// The scale words of 128 rows (of A, or columns of B) from shared to tensor
+// memory: row 32 j + p's word, at byte 16 p + 4 j, goes to lane p of column j, in
+// all four quarters of the lanes.  Runs before the products issued after it and
+// after those issued before it, by the same thread; in both blocks of a pair.
+template <int kCtas>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t to, uint64_t from, bool issue) {
+    if (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(to),
+            "l"(from), "r"((uint32_t)issue)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(to),
+            "l"(from), "r"((uint32_t)issue)
+            : "memory");
+}
+
 // Arrives once on `bar` (of both blocks of a pair) when every product this
 // thread has issued is complete.
 template <int kCtas>
@@ -252,6 +319,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, bool issue) {
         "{\n\t.reg .pred q;\n\t"
         "setp.ne.b32 q, %1, 0;\n\t"
         "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"((uint32_t)issue)
+        : "memory");
+}
+
+// The same with release: what the thread wrote before is seen by who waits.
+__device__ __forceinline__ void mbar_release_cluster(uint32_t bar, bool issue) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
         "r"((uint32_t)issue)
         : "memory");
 }

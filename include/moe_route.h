@@ -540,8 +540,81 @@ MOE_API moe_status moe_expert_gated_gemm(const void *a, const float *a_scale, co
                                          float *q_scale, void *h, moe_stream_t stream);
 
 /*
+ * moe_quantize_mx4 -- rows to 4-bit values with a power-of-two scale per 32
+ * channels: the operand format of the two products below.  A value is an e2m1
+ * code (bit 3 the sign; 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, the first in
+ * the low half; a scale is a byte that stands for 2^(byte - 127), 255 for NaN.
+ * For a block of 32 channels with the largest magnitude m > 0,
+ *     byte = max(floor(log2 m) - 2 + 127, 0)       (0 for m = 0),
+ *     code = e2m1(v * 2^(127 - byte)), to the nearest, ties to the even code, and
+ * 6 where it would be more.  A block with an infinity or a NaN gets byte 255 and
+ * codes 0, and reads back as NaN.
+ *
+ *   x          device [rows, C] of x_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_FP32),
+ *              16-byte aligned.
+ *   rows, C    rows >= 0 (0 enqueues nothing); C a multiple of 32.
+ *   q          device [rows, C/2] bytes, 16-byte aligned: out.
+ *   scale      device [rows, C/32] bytes: out.
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_quantize_mx4(const void *x, moe_dtype x_dtype, int64_t rows, int C, void *q, void *scale,
+                                    moe_stream_t stream);
+
+/*
+ * moe_dequantize_mx4 -- the values such rows stand for, all exact:
+ * MOE_DTYPE_BF16 with the scales applied (a value times a scale past 2^127 is an
+ * infinity; no row of moe_quantize_mx4 has one), or, with scale NULL,
+ * MOE_DTYPE_FP8_E4M3: the codes' own values.
+ *
+ *   q, scale, rows, C   as above; scale NULL for MOE_DTYPE_FP8_E4M3 only.
+ *   out        device [rows, C] of out_dtype, 16-byte aligned: out.
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_dequantize_mx4(const void *q, const void *scale, int64_t rows, int C, moe_dtype out_dtype,
+                                      void *out, moe_stream_t stream);
+
+/*
+ * moe_expert_gemm_mx4 -- the experts' product over rows grouped by expert, in the
+ * 4-bit format above: for row r of expert e, with b over the blocks of 32
+ * channels of C,
+ *     out[r, n] = sum_b sa[r, b] * sw[e, n, b] * sum_{c in b} a[r, c] * w[e, n, c],
+ * all sums in fp32, rounded once.
+ *
+ *   a          device [rows, C/2] bytes, 16-byte aligned; a_scale [rows, C/32].
+ *   w          device [E, N, C/2] bytes, 16-byte aligned; w_scale [E, N, C/32].
+ *   expert_offsets, E, rows, out_dtype, out   as moe_expert_gemm.  Rows no
+ *              expert owns are not written.
+ *   N          a multiple of 16, C a multiple of 32, up to MOE_MAX_EXPERT_DIM.
+ * Scales at 16-byte boundaries (pointers, and C a multiple of 512) load fastest.
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA; a bounded wait
+ * that ran out is moe_get_expert_error's.
+ */
+MOE_API moe_status moe_expert_gemm_mx4(const void *a, const void *a_scale, const void *w, const void *w_scale,
+                                       const int32_t *expert_offsets, int E, int N, int C, int rows,
+                                       moe_dtype out_dtype, void *out, moe_stream_t stream);
+
+/*
+ * moe_expert_gated_gemm_mx4 -- the first product of a gated expert, its gate and
+ * the quantisation of the result for the second product, in one pass: with p the
+ * fp32 result of moe_expert_gemm_mx4's formula for N = 2*I (the gate's I rows of
+ * the weight first),
+ *     v[r, i] = silu(p[r, i]) * p[r, I + i],
+ * and q, q_scale are v in moe_quantize_mx4's format.
+ *
+ *   a, a_scale, w, w_scale, expert_offsets, E, C, rows   as moe_expert_gemm_mx4
+ *              (w [E, 2*I, C/2], w_scale [E, 2*I, C/32]).
+ *   I          a multiple of 32 in 32..MOE_MAX_EXPERT_DIM/2.
+ *   q          device [rows, I/2] bytes, 16-byte aligned: out.
+ *   q_scale    device [rows, I/32] bytes: out.
+ * Errors: as moe_expert_gemm_mx4.
+ */
+MOE_API moe_status moe_expert_gated_gemm_mx4(const void *a, const void *a_scale, const void *w, const void *w_scale,
+                                             const int32_t *expert_offsets, int E, int I, int C, int rows, void *q,
+                                             void *q_scale, moe_stream_t stream);
+
+/*
  * moe_get_expert_error -- SYNCHRONOUS: waits for `stream`, then takes (reads and
- * clears in one step) the current device's error word of the two products above
+ * clears in one step) the current device's error word of the four products above
  * into *host_code: MOE_DEVERR_COPY_TIMEOUT once a bounded wait inside one of
  * their kernels has run out (the kernel then returns with its output
  * unspecified), else 0.  Returns MOE_ERR_TIMEOUT, or MOE_OK (MOE_ERR_CUDA with
@@ -624,6 +697,58 @@ MOE_API moe_status moe_combine_backward(const void *dout, const void *y, const i
  */
 MOE_API moe_status moe_dispatch_backward(const void *drows, const int32_t *tok2row, int T, int K, int H, int64_t rows,
                                          moe_dtype out_dtype, void *dx, moe_stream_t stream);
+
+/*
+ * moe_rms_norm -- the root-mean-square norm in front of a layer, with the
+ * residual's addition: with s = x + residual (x alone without one) in fp32 and
+ * r = 1 / sqrt(mean over h of s^2 + eps),
+ *     y = s * r * weight,   h = s,
+ * each rounded to bf16 once, and, where wanted, y in e4m3 with one fp32 scale per
+ * 128 channels by moe_dispatch's rule, from the unrounded y.
+ *
+ *   x, residual device bf16 [T, H], 16-byte aligned; residual NULL: none.
+ *   weight     device bf16 [H], 16-byte aligned.
+ *   T, H       T >= 0 (0 enqueues nothing); H a multiple of 8 (of 128 with q) in
+ *              8..MOE_MAX_HIDDEN.
+ *   eps        >= 0.
+ *   y          device bf16 [T, H], 16-byte aligned: out.
+ *   h          device bf16 [T, H], 16-byte aligned: out, exactly where residual
+ *              is given.  y or h may be x or residual themselves.
+ *   q, q_scale device e4m3 [T, H], 16-byte aligned, and fp32 [T, H/128]: out, or
+ *              NULL.
+ * The squares are summed in fp32: a row with |s| past about 1.8e19 / sqrt(H)
+ * overflows and gives y = 0 (NaN at an infinity).
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_rms_norm(const void *x, const void *residual, const void *weight, int T, int H, float eps,
+                                void *y, void *h, void *q, float *q_scale, moe_stream_t stream);
+
+/* Bytes of workspace moe_rms_norm_backward needs (0 for T < 1 or a bad H). */
+MOE_API size_t moe_rms_norm_workspace_bytes(int T, int H);
+
+/*
+ * moe_rms_norm_backward -- gradient of moe_rms_norm, from its input (h, or x
+ * without a residual).  With r as there, n = h * r and g = dy * weight,
+ *     dx = r * (g - n * mean over h of (g * n)) + dh,
+ *     dweight = sum over rows of dy * n,
+ * all sums in fp32, in an order that does not change from call to call.  dx is
+ * the gradient of x and of residual alike.  (Quantisation passes gradients
+ * through unchanged.)
+ *
+ *   dy, h      device bf16 [T, H], 16-byte aligned.
+ *   weight     device bf16 [H], 16-byte aligned.
+ *   dh         device bf16 [T, H], 16-byte aligned, or NULL: the gradient that
+ *              reaches h past the norm, added to dx.
+ *   dx         device bf16 [T, H], 16-byte aligned: out; may be dy, h or dh.
+ *   dweight    device fp32 [H]: out (0 for T = 0).
+ *   workspace  device, 16-byte aligned, moe_rms_norm_workspace_bytes(T, H) bytes,
+ *              this call's alone until it is done (NULL for T = 0).
+ * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_WORKSPACE /
+ * MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_rms_norm_backward(const void *dy, const void *h, const void *weight, const void *dh, int T,
+                                         int H, float eps, void *dx, float *dweight, void *workspace,
+                                         size_t workspace_bytes, moe_stream_t stream);
 
 /*
  * moe_get_device_error -- SYNCHRONOUS: waits for `stream`, then copies the

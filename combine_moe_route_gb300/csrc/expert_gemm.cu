@@ -665,7 +665,14 @@ cudaError_t launch_expert_gated_gemm(const void *a, const float *a_scale, const 
 }
 
 cudaError_t product_error_word(int32_t **word) {
-    return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_product_error);
+    static std::atomic<int32_t *> known[64];   // by device: the look-up takes a microsecond
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*word = known[dev].load(std::memory_order_acquire)) != nullptr) return cudaSuccess;
+    e = cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_product_error);
+    if (e == cudaSuccess && dev < 64) known[dev].store(*word, std::memory_order_release);
+    return e;
 }
 
 // Read and cleared in one step: a product on another stream whose wait runs out

@@ -64,8 +64,11 @@ struct Mx4Layout {
     static constexpr int kStages = (227 * 1024 - 4608 - 8 * kStagingWarp - 1024) / kStageBytes;
     static constexpr int kStaging = kStages * kStageBytes;
     static constexpr int kBytes = kStaging + 8 * kStagingWarp + 1024;
-    static constexpr int kAccs = kBN == 128 ? 2 : 1;                    // accumulators in turn
-    static constexpr int kTmemScales = kAccs * kBN;                     // columns from here: 8 per group
+    // Two accumulators in turn.  Of 256 columns they share 48, so that the scales have room:
+    // the next tile starts when the last one's shared columns are read.
+    static constexpr int kShared = kBN == 256 ? 48 : 0;
+    static constexpr int kSecond = kBN - kShared;                       // first column of the second
+    static constexpr int kTmemScales = 2 * kBN - kShared;               // columns from here: 8 per group
 };
 
 template <int kCtas, int kBN>
@@ -270,11 +273,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const uint64_t s0 = scales_descriptor(tiles_at + Layout::kScales);
                 const uint32_t scales = tmem + Layout::kTmemScales;
                 Ring r, acc;
+                bool first = true;
                 for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += stride) {
-                    go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.acc_empty[acc.slot]), acc.parity ^ 1u));
+                    // free: this accumulator's last tile, or the shared columns of the other's
+                    if (Layout::kShared == 0)
+                        go = mbar_wait_polls(at(&s.acc_empty[acc.slot]), acc.parity ^ 1u);
+                    else if (!first)
+                        go = mbar_wait_polls(at(&s.acc_empty[acc.slot ^ 1]), acc.parity ^ (acc.slot ^ 1));
+                    first = false;
+                    go = __all_sync(0xffffffffu, go);
                     if (!go) break;
                     tcgen05_fence_after();
-                    const uint32_t d = tmem + acc.slot * kBN;
+                    const uint32_t d = tmem + acc.slot * Layout::kSecond;
                     for (int kb = 0; kb < nk; ++kb) {
                         const bool full = mbar_wait_polls(at(&s.full[r.slot]), r.parity);
                         tcgen05_fence_after();
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         if (!go) break;
                     }
                     mma_commit<kCtas>(at(&s.acc_full[acc.slot]), issue);
-                    acc.advance(Layout::kAccs);
+                    acc.advance(2);
                 }
                 if (!go) {   // leave no product running
                     mma_commit<kCtas>(at(&s.drain), issue);
@@ -394,20 +404,53 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 uint32_t r[kHalves * 4][16];
                 go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.acc_full[acc.slot]), acc.parity));
                 tcgen05_fence_after();
+                const uint32_t from = lanes + acc.slot * Layout::kSecond;
+                const auto load = [&](int first, int end) {   // of 16 columns each
+#pragma unroll
+                    for (int k = 0; k < kHalves * 4; ++k)
+                        if (k >= first && k < end) tmem_load(from + (k / 4) * kApart + (k & 3) * 16, r[k]);
+                };
+                const auto wait = [&](int first, int end) {
+#pragma unroll
+                    for (int k = 0; k < kHalves * 4; ++k)
+                        if (k >= first && k < end) tmem_wait_load(r[k]);
+                };
+                const auto free = [&] {   // what is read by now may be written
+                    tcgen05_fence_before();
+                    if (kCtas == 2) mbar_arrive_cluster(first_empty + acc.slot * 8, issue);
+                    else mbar_arrive(at(&s.acc_empty[acc.slot]), issue);
+                };
+                if constexpr (Layout::kShared == 0) {
+                    load(0, kHalves * 4);
+                    wait(0, kHalves * 4);
+                    free();
+                } else {
+                    // the shared columns first: the last 48 of the first accumulator are the second
+                    // warpgroup's, the first 48 of the second one the first's
+                    if (acc.slot == 0 && wg == 1) {
+                        load(5, 8);
+                        wait(5, 8);
+                        free();
+                        load(0, 5);
+                        wait(0, 5);
+                    } else if (acc.slot == 1 && wg == 0) {
+                        load(0, 3);
+                        wait(0, 3);
+                        free();
+                        load(3, 8);
+                        wait(3, 8);
+                    } else {
+                        free();
+                        load(0, 8);
+                        wait(0, 8);
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < kHalves * 4; ++k)
-                    tmem_load(lanes + acc.slot * kBN + (k / 4) * kApart + (k & 3) * 16, r[k]);
-#pragma unroll
-                for (int k = 0; k < kHalves * 4; ++k) {
-                    tmem_wait_load(r[k]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         v[k * 8 + j] = make_float2(__uint_as_float(r[k][2 * j]), __uint_as_float(r[k][2 * j + 1]));
-                }
-                tcgen05_fence_before();   // all read: the accumulator is free
-                if (kCtas == 2) mbar_arrive_cluster(first_empty + acc.slot * 8, issue);
-                else mbar_arrive(at(&s.acc_empty[acc.slot]), issue);
-                acc.advance(Layout::kAccs);
+                acc.advance(2);
             }
             uint32_t keep;   // rows of this warp that are this block's to write: a mask (kSplit) or how many
             if constexpr (kSplit) {
@@ -566,6 +609,14 @@ static cudaError_t launch_mx4(const void *a, const void *w, Mx4Args p, cudaStrea
         return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
     };
     p.a_width = width(p.a_scale), p.w_width = width(p.w_scale);
+#ifndef NO_PAIRS
+    if (p.rows > (long long)p.E * kRowTile) {
+        e = launch_mx4_tiles<2, 256, kGated>(a, w, p, stream);
+        if (e != cudaSuccess) return e;
+        p.tails = true;
+        return launch_mx4_tiles<1, 256, kGated>(a, w, p, stream);
+    }
+#endif
     const long long row_tiles = (long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E);   // at most
     constexpr int kNarrow = kGated ? 256 : 128;
     p.split = mx4_split_parts(row_tiles * ((p.N + kNarrow - 1) / kNarrow), p.C);

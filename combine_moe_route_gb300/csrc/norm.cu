@@ -11,8 +11,11 @@
 //
 // A team of 32, 128 or 256 threads holds a row in registers, 8 channels a chunk,
 // so that it is read once; 16 neighbouring lanes hold a block of 128 channels.
+#include <algorithm>
+#include <atomic>
+
 #include "launch.h"
-#include "numeric.cuh"
+#include "product.cuh"
 
 namespace moe {
 
@@ -160,89 +163,255 @@ cudaError_t launch_rms_norm(const void *x, const void *residual, const void *wei
 // --------------------------------------------------------------------------
 // gradient
 // --------------------------------------------------------------------------
-// Teams walk the rows; each keeps its sums of dweight in registers and leaves
-// them as a row of the workspace, which a second kernel adds up in order.
-constexpr int kNormGrid = 456;   // blocks at most: three on each of 152 SMs
+// Two sums over a row (of h^2 and of g * h) stand between its reads and its writes,
+// and dweight needs every row.  Blocks walk the rows; each thread keeps the dweight
+// of its channels in registers, the blocks leave theirs as rows of the workspace,
+// and a second kernel adds those up in order.
+//
+// Rows past 1024 channels are a whole block's.  Their bulk copies go through a ring
+// of stages in shared memory, so that the next rows are on their way while a row
+// waits for its sums; a stage is free again at the sums' barrier, when its values
+// are in registers.  Shorter rows are a warp's, read one row ahead.
+constexpr int kGradTeam = 256;           // threads of a block
+constexpr int kGradStages = 8;           // rows of a ring at most
+constexpr int kNormSms = 152;            // the grids below are sized for
 
-template <int kTeam, int kChunks>
-__global__ void __launch_bounds__(norm_threads<kTeam>(), 2) rms_norm_backward_kernel(
-    const __nv_bfloat16 *dy, const __nv_bfloat16 *h, const __nv_bfloat16 *weight, const __nv_bfloat16 *dh, long long T,
-    int H, float eps, __nv_bfloat16 *dx, float *partial) {
-    constexpr int kTeams = norm_threads<kTeam>() / kTeam;
-    __shared__ float s_part[2][norm_threads<kTeam>() / 32][2];
-    const int nchunk = H / 8, at = threadIdx.x % kTeam;
-    const long long team = (long long)blockIdx.x * kTeams + threadIdx.x / kTeam;
+struct NormGradArgs {
+    const __nv_bfloat16 *dy, *h, *weight, *dh;
+    long long T;
+    int H;
+    float eps;
+    __nv_bfloat16 *dx;
+    float *partial;     // [blocks, H], or dweight itself (one cluster)
+    int stages;
+    int32_t *error;
+};
+
+// A chunk's part of the two sums.
+__device__ __forceinline__ void add_sums(const uint4 h, const uint4 dy, const uint4 w, float2 (&sum)[2]) {
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w}, d[4] = {dy.x, dy.y, dy.z, dy.w}, g[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 v = bf16_pair_floats(a[k]);
+        fma_pair(sum[0], v, v);
+        fma_pair(sum[1], mul_pair(bf16_pair_floats(d[k]), bf16_pair_floats(g[k])), v);
+    }
+}
+
+// A chunk of dx, and its part of dweight.  r and m: 1 / the norm, and what of h is
+// taken from g, mean(g n) r.
+__device__ __forceinline__ uint4 chunk_gradient(const uint4 h, const uint4 dy, const uint4 w, const uint4 dh, float r,
+                                                float m, float2 (&acc)[4]) {
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w}, d[4] = {dy.x, dy.y, dy.z, dy.w}, g[4] = {w.x, w.y, w.z, w.w},
+                   o[4] = {dh.x, dh.y, dh.z, dh.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 v = bf16_pair_floats(a[k]), e = bf16_pair_floats(d[k]);
+        fma_pair(acc[k], e, mul_pair(v, make_float2(r, r)));
+        float2 t = mul_pair(e, bf16_pair_floats(g[k]));
+        fma_pair(t, v, make_float2(-m, -m));
+        float2 x = bf16_pair_floats(o[k]);
+        fma_pair(x, t, make_float2(r, r));
+        out[k] = bf16_pair(x.x, x.y);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <int kChunks>
+__global__ void __launch_bounds__(kGradTeam, kChunks <= 4 ? 2 : 1) norm_gradient_kernel(const NormGradArgs p) {
+    extern __shared__ unsigned char s_raw[];
+    __shared__ __align__(8) uint64_t s_full[kGradStages];
+    __shared__ float s_part[2][kGradTeam / 32][2];
+    const int H = p.H, nchunk = H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t row_bytes = (uint32_t)H * 2, stage_bytes = row_bytes * (p.dh ? 3 : 2);
+    const uint32_t tiles = (smem_u32(s_raw) + 15u) & ~15u;
+    unsigned char *tiles_p = s_raw + (tiles - smem_u32(s_raw));
+    const auto fetch = [&](int stage, long long row) {   // one thread
+        mbar_arrive_expect_tx(&s_full[stage], stage_bytes);
+        unsigned char *to = tiles_p + stage * stage_bytes;
+        bulk_load(to, p.h + (size_t)row * H, row_bytes, &s_full[stage]);
+        bulk_load(to + row_bytes, p.dy + (size_t)row * H, row_bytes, &s_full[stage]);
+        if (p.dh) bulk_load(to + 2 * row_bytes, p.dh + (size_t)row * H, row_bytes, &s_full[stage]);
+    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) mbar_init(&s_full[i], 1);
+        fence_mbarrier_init();
+    }
     pdl_launch_dependents();
     pdl_wait();
-    float acc[kChunks][8];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
-    int turn = 0;   // the sums' slots alternate, so that one barrier a row is enough
-    for (long long row = team; row < T; row += (long long)gridDim.x * kTeams, turn ^= 1) {
-        const size_t from = (size_t)row * H;
-        uint4 hv[kChunks], gv[kChunks];
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int c = at + i * kTeam;
-            hv[i] = c < nchunk ? ld_chained_v4(h + from + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-            gv[i] = c < nchunk ? ld_chained_v4(dy + from + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int i = 0; i < p.stages; ++i) {
+            const long long row = blockIdx.x + (long long)i * gridDim.x;
+            if (row < p.T) fetch(i, row);
         }
-        float sum[2] = {0.0f, 0.0f};   // of h^2 and of g * h
+    uint4 w[kChunks];
+    float2 acc[kChunks][4];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = threadIdx.x + i * kGradTeam;
+        w[i] = c < nchunk ? ld_cached_v4(p.weight + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] = make_float2(0.0f, 0.0f);
+    }
+    int stage = 0, turn = 0;   // the sums' slots alternate, so that one barrier a row is enough
+    uint32_t parity = 0;
+    bool ok = true;
+    for (long long row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
+        ok = mbar_wait_polls(smem_u32(&s_full[stage]), parity);
+        uint4 h[kChunks], dy[kChunks], dh[kChunks];
+        const uint32_t from = tiles + stage * stage_bytes;
+        float2 two[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int c = at + i * kTeam;
-            float a[8], d[8], w[8];
-            unpack_bf16x8(hv[i], a);
-            unpack_bf16x8(gv[i], d);
-            unpack_bf16x8(c < nchunk ? ld_cached_v4(weight + c * 8) : make_uint4(0u, 0u, 0u, 0u), w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                sum[0] = fmaf(a[k], a[k], sum[0]);
-                sum[1] = fmaf(d[k] * w[k], a[k], sum[1]);
-            }
+            const int c = threadIdx.x + i * kGradTeam;
+            h[i] = dy[i] = dh[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c >= nchunk) continue;
+            h[i] = ld_shared_v4(from + c * 16);
+            dy[i] = ld_shared_v4(from + row_bytes + c * 16);
+            if (p.dh) dh[i] = ld_shared_v4(from + 2 * row_bytes + c * 16);
+            add_sums(h[i], dy[i], w[i], two);
         }
-        team_sums<kTeam, 2>(sum, s_part[turn]);
-        const float r = rsqrtf(sum[0] / (float)H + eps);
-        const float m = sum[1] / (float)H * r * r;   // mean(g n) r: of h * r taken from g
+        float sum[2] = {two[0].x + two[0].y, two[1].x + two[1].y};
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
+            sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], off);
+        }
+        if (lane == 0) s_part[turn][warp][0] = sum[0], s_part[turn][warp][1] = sum[1];
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        if (threadIdx.x == 0) {   // everyone has this stage's values: the ring's next row
+            const long long next = row + (long long)p.stages * gridDim.x;
+            if (next < p.T) fetch(stage, next);
+        }
+        if (++stage == p.stages) stage = 0, parity ^= 1u;
+        sum[0] = sum[1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kGradTeam / 32; ++i) sum[0] += s_part[turn][i][0], sum[1] += s_part[turn][i][1];
+        const float r = rsqrtf(sum[0] / (float)H + p.eps), m = sum[1] / (float)H * r * r;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int c = at + i * kTeam;
-            if (c >= nchunk) break;
-            float a[8], d[8], w[8], o[8];
-            if (dh) unpack_bf16x8(ld_chained_v4(dh + from + c * 8), o);
-            unpack_bf16x8(hv[i], a);
-            unpack_bf16x8(gv[i], d);
-            unpack_bf16x8(ld_cached_v4(weight + c * 8), w);
+            const int c = threadIdx.x + i * kGradTeam;
+            if (c < nchunk)
+                st_v4(p.dx + (size_t)row * H + c * 8, chunk_gradient(h[i], dy[i], w[i], dh[i], r, m, acc[i]));
+        }
+    }
+    if (!ok) {   // a copy did not come: leave none in flight, if they come at all
+        if (threadIdx.x == 0) {
+            atomicOr(p.error, MOE_DEVERR_COPY_TIMEOUT);
+            for (int i = 0; i < p.stages; ++i) mbar_wait_polls(smem_u32(&s_full[i]), i < stage ? parity ^ 1u : parity);
+        }
+        return;
+    }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                acc[i][k] = fmaf(d[k], a[k] * r, acc[i][k]);
-                const float t = r * (d[k] * w[k] - a[k] * m);
-                o[k] = dh ? t + o[k] : t;
-            }
-            st_v4(dx + from + c * 8, pack_bf16x8(o));
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = threadIdx.x + i * kGradTeam;
+        if (c >= nchunk) break;
+        float4 *to = reinterpret_cast<float4 *>(p.partial + (size_t)blockIdx.x * H + c * 8);
+        to[0] = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+        to[1] = make_float4(acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y);
+    }
+}
+
+// Rows of up to 1024 channels, one a warp.  kCluster: the grid is one cluster, whose
+// blocks add their sums through shared memory and write dweight.
+template <int kChunks, bool kCluster>
+__global__ void __launch_bounds__(kGradTeam) norm_gradient_warps_kernel(const NormGradArgs p) {
+    extern __shared__ float s_sums[];   // [warps, H]
+    constexpr int kWarps = kGradTeam / 32;
+    const int H = p.H, nchunk = H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    uint4 w[kChunks], h[kChunks], dy[kChunks], dh[kChunks];
+    float2 acc[kChunks][4];
+    const auto load = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = lane + i * 32;
+            h[i] = dy[i] = dh[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c >= nchunk || row >= p.T) continue;
+            const size_t at = (size_t)row * H + c * 8;
+            h[i] = ld_chained_v4(p.h + at);
+            dy[i] = ld_chained_v4(p.dy + at);
+            if (p.dh) dh[i] = ld_chained_v4(p.dh + at);
+        }
+    };
+    const long long step = (long long)gridDim.x * kWarps;
+    long long row = (long long)blockIdx.x * kWarps + warp;
+    load(row);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = lane + i * 32;
+        w[i] = c < nchunk ? ld_cached_v4(p.weight + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] = make_float2(0.0f, 0.0f);
+    }
+    for (; row < p.T; row += step) {
+        uint4 a[kChunks], d[kChunks], o[kChunks];
+        float2 two[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            a[i] = h[i], d[i] = dy[i], o[i] = dh[i];
+            add_sums(a[i], d[i], w[i], two);
+        }
+        load(row + step);   // in flight over this row's sums
+        float sum[2] = {two[0].x + two[0].y, two[1].x + two[1].y};
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
+            sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], off);
+        }
+        const float r = rsqrtf(sum[0] / (float)H + p.eps), m = sum[1] / (float)H * r * r;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = lane + i * 32;
+            if (c < nchunk)
+                st_v4(p.dx + (size_t)row * H + c * 8, chunk_gradient(a[i], d[i], w[i], o[i], r, m, acc[i]));
         }
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-        const int c = at + i * kTeam;
+        const int c = lane + i * 32;
         if (c >= nchunk) break;
-        float4 *to = reinterpret_cast<float4 *>(partial + (size_t)team * H + c * 8);
-        to[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        to[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+        float4 *to = reinterpret_cast<float4 *>(s_sums + warp * H + c * 8);
+        to[0] = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+        to[1] = make_float4(acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < H; c += kGradTeam) {
+        float sum = s_sums[c];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) sum += s_sums[i * H + c];
+        if (kCluster) s_sums[c] = sum;   // this thread's column alone
+        else p.partial[(size_t)blockIdx.x * H + c] = sum;
+    }
+    if constexpr (kCluster) {
+        cluster_barrier();
+        const int blocks = gridDim.x, mine = (H + blocks - 1) / blocks;
+        for (int i = threadIdx.x; i < mine; i += kGradTeam) {
+            const int c = blockIdx.x * mine + i;
+            if (c >= H) break;
+            float sum = 0.0f;
+            for (int b = 0; b < blocks; ++b) sum += ld_cluster(block_address(smem_u32(s_sums + c), b));
+            p.partial[c] = sum;
+        }
+        cluster_barrier();   // a block's sums are read until here
     }
 }
 
-// Columns of the partial rows: 32 a block, its 8 warps a run of rows each.
+// Columns of the partial rows: 32 a block, its 8 warps every eighth row each.
 __global__ void __launch_bounds__(256) norm_columns_kernel(const float *partial, int parts, int H, float *dweight) {
     __shared__ float s_sum[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     pdl_launch_dependents();
     pdl_wait();
     float sum = 0.0f;
-    if (c < H)
+    if (c < H) {
+#pragma unroll 8
         for (int i = warp; i < parts; i += 8) sum += ld_chained(partial + (size_t)i * H + c);
+    }
     s_sum[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && c < H) {
@@ -252,57 +421,80 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const float *partial,
     }
 }
 
-static int team_of(int H) { return H <= 32 * 4 * 8 ? 32 : H <= 128 * 8 * 8 ? 128 : 256; }
-static int teams_a_block(int H) { return team_of(H) == 32 ? 4 : 1; }
+// Rows that a warp takes, and up to how many of them one cluster of 8 blocks does
+// alone: 8 rows a warp.
+static bool short_rows(int H) { return H <= 1024; }
+static bool one_cluster(long long T, int H) { return short_rows(H) && T <= 8 * 8 * 8; }
+
 static int norm_grid(long long T, int H) {
-    const int teams = teams_a_block(H);
-    const long long blocks = (T + teams - 1) / teams;
-    return (int)(blocks < kNormGrid ? blocks : kNormGrid);
+    const int rows = short_rows(H) ? kGradTeam / 32 : 1;
+    const int most = one_cluster(T, H) ? 8 : kNormSms * (H <= 8192 ? 2 : 1);
+    const long long blocks = (T + rows - 1) / rows;
+    return (int)(blocks < most ? blocks : most);
 }
 
 size_t norm_workspace_bytes(long long T, int H) {
-    return (size_t)norm_grid(T, H) * teams_a_block(H) * H * sizeof(float);
+    return one_cluster(T, H) ? 0 : (size_t)norm_grid(T, H) * H * sizeof(float);
 }
 
-template <int kTeam, int kChunks>
-static cudaError_t launch_norm_backward(const void *dy, const void *h, const void *weight, const void *dh, long long T,
-                                        int H, float eps, void *dx, float *partial, cudaStream_t stream) {
-    return launch_chained(rms_norm_backward_kernel<kTeam, kChunks>, (unsigned)norm_grid(T, H), norm_threads<kTeam>(), 0,
-                          stream, static_cast<const __nv_bfloat16 *>(dy), static_cast<const __nv_bfloat16 *>(h),
-                          static_cast<const __nv_bfloat16 *>(weight), static_cast<const __nv_bfloat16 *>(dh), T, H, eps,
-                          static_cast<__nv_bfloat16 *>(dx), partial);
+template <int kChunks>
+static cudaError_t launch_long_rows(NormGradArgs p, int grid, cudaStream_t stream) {
+    const cudaError_t e = product_error_word(&p.error);
+    if (e != cudaSuccess) return e;
+    auto kernel = norm_gradient_kernel<kChunks>;
+    const int stage = p.H * (p.dh ? 6 : 4), room = (kChunks <= 4 ? 113 : 226) * 1024 - 512;
+    p.stages = std::min(room / stage, kGradStages);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t r = raise_shared_limit(reinterpret_cast<const void *>(kernel), room, ready);
+    if (r != cudaSuccess) return r;
+    return launch_chained(kernel, (unsigned)grid, kGradTeam, (size_t)(p.stages * stage + 16), stream, p);
 }
 
-static cudaError_t launch_rows_backward(const void *dy, const void *h, const void *weight, const void *dh, long long T,
-                                        int H, float eps, void *dx, float *partial, cudaStream_t stream) {
-    const int nchunk = H / 8;
-#define MOE_NORM(team, chunks) \
-    if (nchunk <= team * chunks) \
-        return launch_norm_backward<team, chunks>(dy, h, weight, dh, T, H, eps, dx, partial, stream)
-    MOE_NORM(32, 1);
-    MOE_NORM(32, 2);
-    MOE_NORM(32, 4);
-    MOE_NORM(128, 2);
-    MOE_NORM(128, 3);
-    MOE_NORM(128, 4);
-    MOE_NORM(128, 5);
-    MOE_NORM(128, 6);
-    MOE_NORM(128, 7);
-    MOE_NORM(128, 8);
-    MOE_NORM(256, 6);
-    MOE_NORM(256, 8);
-#undef MOE_NORM
-    return cudaErrorInvalidValue;
+template <int kChunks>
+static cudaError_t launch_short_rows(const NormGradArgs &p, int grid, bool cluster, cudaStream_t stream) {
+    const size_t smem = (size_t)p.H * (kGradTeam / 32) * sizeof(float);   // 32 KB at most
+    if (!cluster) return launch_chained(norm_gradient_warps_kernel<kChunks, false>, (unsigned)grid, kGradTeam, smem, stream, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kGradTeam);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)grid;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, norm_gradient_warps_kernel<kChunks, true>, p);
 }
 
 cudaError_t launch_rms_norm_backward(const void *dy, const void *h, const void *weight, const void *dh, long long T,
                                      int H, float eps, void *dx, float *dweight, void *workspace, cudaStream_t stream) {
     if (T == 0) return cudaMemsetAsync(dweight, 0, (size_t)H * sizeof(float), stream);
-    float *partial = static_cast<float *>(workspace);
-    const cudaError_t e = launch_rows_backward(dy, h, weight, dh, T, H, eps, dx, partial, stream);
-    if (e != cudaSuccess) return e;
+    NormGradArgs p = {};
+    p.dy = static_cast<const __nv_bfloat16 *>(dy), p.h = static_cast<const __nv_bfloat16 *>(h);
+    p.weight = static_cast<const __nv_bfloat16 *>(weight), p.dh = static_cast<const __nv_bfloat16 *>(dh);
+    p.T = T, p.H = H, p.eps = eps, p.dx = static_cast<__nv_bfloat16 *>(dx);
+    const bool cluster = one_cluster(T, H);
+    p.partial = cluster ? dweight : static_cast<float *>(workspace);
+    const int grid = norm_grid(T, H), chunks = (H / 8 + (short_rows(H) ? 31 : kGradTeam - 1)) / (short_rows(H) ? 32 : kGradTeam);
+    cudaError_t e;
+    if (short_rows(H))
+        e = chunks == 1   ? launch_short_rows<1>(p, grid, cluster, stream)
+            : chunks == 2 ? launch_short_rows<2>(p, grid, cluster, stream)
+                          : launch_short_rows<4>(p, grid, cluster, stream);
+    else
+        e = chunks == 1   ? launch_long_rows<1>(p, grid, stream)
+            : chunks == 2 ? launch_long_rows<2>(p, grid, stream)
+            : chunks == 3 ? launch_long_rows<3>(p, grid, stream)
+            : chunks == 4 ? launch_long_rows<4>(p, grid, stream)
+            : chunks <= 6 ? launch_long_rows<6>(p, grid, stream)
+                          : launch_long_rows<8>(p, grid, stream);
+    if (e != cudaSuccess || cluster) return e;
     return launch_chained(norm_columns_kernel, (unsigned)((H + 31) / 32), 256, 0, stream,
-                          static_cast<const float *>(partial), norm_grid(T, H) * teams_a_block(H), H, dweight);
+                          static_cast<const float *>(p.partial), grid, H, dweight);
 }
 
 }  // namespace moe

@@ -306,6 +306,11 @@ __device__ __forceinline__ uint32_t block_address(uint32_t p, uint32_t rank) {
 }
 __device__ __forceinline__ uint32_t first_block_address(uint32_t p) { return block_address(p, 0); }
 
+__device__ __forceinline__ float ld_cluster(uint32_t p) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+    return v;
+}
 __device__ __forceinline__ void st_cluster_v4(uint32_t p, float4 v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");

@@ -13,10 +13,10 @@
 //                tiled bulk tensor copies into a ring of stages;
 //   warp 9       copies a stage's scales to tensor memory and issues its products
 //                (4 x K = 64);
-//   warps 10, 11 take turns at bringing the scales of two stages from their rows
-//                (16 bytes each) to the order the tensor cores want: 128 rows' words
-//                of four scales, row 32 j + p at byte 16 p + 4 j, so that a lane
-//                holds the words of four rows and writes 16 bytes;
+//   warps 10-15  bring the scales from their rows to the order the tensor cores want:
+//                128 rows' words of four scales, row 32 j + p at byte 16 p + 4 j.  Two
+//                warps a group of 128 rows, of A or of the weight, 64 rows each; a lane
+//                reads 32 bytes of a row, four stages', at once;
 //   warps 0-7    (two warpgroups) read a finished tile, one row per thread and half
 //                of its columns per warpgroup, and write it, or form silu(g) * u and
 //                quantise it: a block of 32 channels is one thread's.
@@ -30,13 +30,15 @@
 
 namespace moe {
 
-// Registers of a thread of the loading, issuing and scaling warpgroup and of the
-// two others, out of the 168 that a block of 384 threads starts with:
-// 104 + 2 * 200 = 3 * 168.
-constexpr int kMx4FeedRegisters = 104, kMx4OutRegisters = 200;
+constexpr int kMx4Threads = 512;
+// Registers of a thread of the two warpgroups that load, issue and bring scales and
+// of the two others, out of the 128 that a block of 512 threads starts with:
+// 2 * 64 + 2 * 192 = 4 * 128.
+constexpr int kMx4FeedRegisters = 64, kMx4OutRegisters = 192;
 constexpr int kMx4K = 256;                      // channels per stage: 128 bytes of a row
 constexpr int kMx4StageA = kRowTile * kMx4K / 2;
 constexpr int kScaleTile = 512;                 // bytes: the words of 128 rows, four scales each
+constexpr int kScaleRun = 4;                    // stages whose scales a warp loads at once
 
 struct Mx4Args {
     const unsigned char *a_scale, *w_scale;
@@ -77,7 +79,7 @@ struct Mx4Shared {
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem;
-    int32_t warp_tiles[kProductThreads / 32];
+    int32_t warp_tiles[kMx4Threads / 32];
     int32_t tiles[MOE_MAX_EXPERTS + 1];    // row tiles before expert e
 };
 
@@ -92,22 +94,36 @@ __device__ __forceinline__ int mx4_row_tiles(const Mx4Args &p, int n) {
     return (n + kRowTile - 1) / kRowTile;
 }
 
+// A block's way through its tiles: experts in order; within an expert the row tiles
+// of one column tile come first, so that blocks working at the same time share the
+// weight.  What the next tile shares with the last one is kept: every role that walks
+// looks for an expert only when it leaves one.
 struct Mx4Tile {
-    int e, row0, valid, n;   // expert, this block's first row and rows, column tile
+    long long t;             // tile
+    int e, mt;               // expert and its row tiles
+    long long begin, end;    // its tiles
+    int2 rows;               // its first row and rows
+    int row0, valid, n;      // this block's first row and rows, column tile
     int pair_valid;          // rows of the blocks together
 };
 
-// Tile t: experts in order; within an expert the row tiles of one column tile
-// come first, so that blocks working at the same time share the weight.
 template <int kCtas, class Shared>
-__device__ __forceinline__ Mx4Tile mx4_tile(const Shared &s, const Mx4Args &p, long long t, int rank) {
-    const int e = upper_bound_minus_one(s.tiles, p.E, (int)(t / p.ntiles));
-    const int mt = s.tiles[e + 1] - s.tiles[e];
-    const int i = (int)(t - (long long)s.tiles[e] * p.ntiles);
-    const int2 r = expert_rows(p, e);
-    const int m = kCtas == 1 && p.tails ? r.y / (2 * kRowTile) * 2 : i % mt * kCtas;   // in units of 128 rows
-    const int valid = min(r.y - m * kRowTile, kCtas * kRowTile);
-    return {e, r.x + (m + rank) * kRowTile, max(min(valid - rank * kRowTile, kRowTile), 0), i / mt, valid};
+__device__ __forceinline__ void mx4_go(Mx4Tile &w, const Shared &s, const Mx4Args &p, long long t, int rank) {
+    w.t = t;
+    if (t >= w.end) {
+        w.e = upper_bound_minus_one(s.tiles, p.E, (int)(t / p.ntiles));
+        w.mt = s.tiles[w.e + 1] - s.tiles[w.e];
+        w.begin = (long long)s.tiles[w.e] * p.ntiles;
+        w.end = w.begin + (long long)w.mt * p.ntiles;
+        w.rows = expert_rows(p, w.e);
+    }
+    const uint32_t i = (uint32_t)(t - w.begin);   // an expert's tiles: under 2^32 (2^24 row tiles of 2^8 column tiles)
+    w.n = (int)(i / (uint32_t)w.mt);
+    const int m = kCtas == 1 && p.tails ? w.rows.y / (2 * kRowTile) * 2
+                                        : (int)(i - (uint32_t)w.n * w.mt) * kCtas;   // in units of 128 rows
+    w.pair_valid = min(w.rows.y - m * kRowTile, kCtas * kRowTile);
+    w.row0 = w.rows.x + (m + rank) * kRowTile;
+    w.valid = max(min(w.pair_valid - rank * kRowTile, kRowTile), 0);
 }
 
 // 16 scales of a row, those past its end as 0 (their channels are 0 too).
@@ -134,7 +150,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
 }
 
 template <int kCtas, int kBN, bool kGated, bool kSplit>
-__global__ void __launch_bounds__(kProductThreads, 1)
+__global__ void __launch_bounds__(kMx4Threads, 1)
     expert_mx4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_few,
                       const __grid_constant__ CUtensorMap map_w, const Mx4Args p) {
     using Layout = Mx4Layout<kCtas, kBN>;
@@ -147,14 +163,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
     const int nkb = (p.C + kMx4K - 1) / kMx4K;
     const int parts = kSplit ? p.split : 1, part = kSplit ? (int)cluster_rank() : 0;
-    // this block's channels, from an even stage on: a load of scales is two stages' and stays aligned
+    // this block's channels, from an even stage on: 16 scales' loads stay aligned
     const int kb_first = kSplit ? (nkb + 1) / 2 * part / parts * 2 : 0;
     const int nk = kSplit ? min((nkb + 1) / 2 * (part + 1) / parts * 2, nkb) - kb_first : nkb;
 
     // prologue: barriers, tensor memory, and the experts' row tiles
     if (threadIdx.x == 0) {
         for (int i = 0; i < Layout::kStages; ++i) {
-            mbar_init(&s.full[i], 1 + kCtas);   // the loads' bytes, each block's scales
+            mbar_init(&s.full[i], 1 + kCtas * 2 * Layout::kGroups);   // the loads' bytes, each block's scales
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -173,7 +189,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     pdl_launch_dependents();
     pdl_wait();
     {
-        constexpr int kPer = (MOE_MAX_EXPERTS + kProductThreads - 1) / kProductThreads;
+        constexpr int kPer = (MOE_MAX_EXPERTS + kMx4Threads - 1) / kMx4Threads;
         int mine = 0, mt[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -220,8 +236,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             // ---------------------------------------------------- loads
             Ring r;
             long long issued = 0;
+            Mx4Tile tile = {};
             for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += stride) {
-                const Mx4Tile tile = mx4_tile<kCtas>(s, p, t, rank);
+                mx4_go<kCtas>(tile, s, p, t, rank);
                 // a pair splits the columns: each block brings half of them; the gate's and the
                 // up projection's lie apart
                 constexpr int kBox = kGated ? 128 : kBN / kCtas, kBoxBytes = kBox * kMx4K / 2;
@@ -287,6 +304,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     const uint32_t d = tmem + acc.slot * Layout::kSecond;
                     for (int kb = 0; kb < nk; ++kb) {
                         const bool full = mbar_wait_polls(at(&s.full[r.slot]), r.parity);
+                        if (kCtas == 2) fence_acquire_shared_cluster();   // the other block's scales
                         tcgen05_fence_after();
                         const uint64_t step = (uint32_t)r.slot * (Layout::kStageBytes >> 4);
                         // group g's scales of the stage's first and second 128 channels: columns
@@ -315,69 +333,70 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
         } else {
             // --------------------------------------------------- scales
-            // Two stages at a time, this warp every other time; the loads of its next time are
-            // in flight while it waits for the stages of this one to be free.
-            const int turn = warp - 10;
-            const int a_bytes = p.C / kMx4Block;
+            // Two warps a group, each the words of 64 rows (two a lane) of every stage; the loads of
+            // the next run of stages are in flight while this one's wait for free stages.
+            // (A warp has to wait for every pass of a stage: a barrier tells a phase from the one
+            // before it only, so warps that took turns at runs could find a stage free that had not
+            // been filled.)
+            const int group = (warp - 10) % Layout::kGroups, half = (warp - 10) / Layout::kGroups;
+            const int bytes = p.C / kMx4Block;
             const uint32_t full0 = kCtas == 2 ? first_block_address(at(&s.full[0])) : 0;
-            Ring r;
-            long long t = blockIdx.x / (kCtas * parts);
+            long long t = half < 2 ? blockIdx.x / (kCtas * parts) : total;
             int kb = 0;
             Mx4Tile tile = {};
-            if (t < total) tile = mx4_tile<kCtas>(s, p, t, rank);
-            const auto step = [&] {   // to the next two stages
-                for (int i = 0; i < 2 && kb < nk; ++i, ++kb) r.advance(Layout::kStages);
-                if (kb < nk) return;
-                kb = 0;
-                t += stride;
-                if (t < total) tile = mx4_tile<kCtas>(s, p, t, rank);
-            };
-            uint4 v[Layout::kGroups][4];
-            const auto load = [&] {
+            if (t < total) mx4_go<kCtas>(tile, s, p, t, rank);
+            uint4 next[2][2];
+            const auto load = [&] {   // the next run's; gives its stages
+                if (t >= total) return 0;
                 const int byte = (kb_first + kb) * (kMx4K / kMx4Block);
+                const int first = group == 0 ? tile.row0
+                                             : tile.n * kTileColumns + (group - 1) * (kGated ? p.N / 2 : 128);
+                const int rows = group == 0 ? tile.valid : kRowTile;
+                const unsigned char *from = (group == 0 ? p.a_scale : p.w_scale + (size_t)tile.e * p.N * bytes) + byte;
+                const int width = group == 0 ? p.a_width : p.w_width, last = group == 0 ? p.rows - 1 : p.N - 1;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int row = q * 32 + lane;
-                    v[0][q] = row < tile.valid
-                                  ? load_scales(p.a_scale + (size_t)(tile.row0 + row) * a_bytes + byte, a_bytes - byte,
-                                                p.a_width)
-                                  : make_uint4(0u, 0u, 0u, 0u);
+                for (int q = 0; q < 2; ++q) {
+                    const int row = (half * 2 + q) * 32 + lane;
+                    const unsigned char *at_row = from + (size_t)min(first + row, last) * bytes;
 #pragma unroll
-                    for (int g = 1; g < Layout::kGroups; ++g) {
-                        const int column = tile.n * kTileColumns + row + (g - 1) * (kGated ? p.N / 2 : 128);
-                        v[g][q] = load_scales(
-                            p.w_scale + ((size_t)tile.e * p.N + min(column, p.N - 1)) * a_bytes + byte, a_bytes - byte,
-                            p.w_width);
-                    }
+                    for (int h = 0; h < 2; ++h)
+                        next[q][h] = load_scales(at_row + h * 16, row < rows ? bytes - byte - h * 16 : 0, width);
                 }
+                const int count = min(kScaleRun, nk - kb);
+                kb += count;
+                if (kb == nk) {
+                    kb = 0;
+                    t += stride;
+                    if (t < total) mx4_go<kCtas>(tile, s, p, t, rank);
+                }
+                return count;
             };
-            if (turn == 1 && t < total) step();
-            if (t < total) load();
-            while (go && t < total) {
-                const int count = min(2, nk - kb);
-                Ring c = r;
+            Ring r;
+            for (int count = load(); go && count > 0;) {
+                const uint4 v[2][2] = {{next[0][0], next[0][1]}, {next[1][0], next[1][1]}};
+                const int after = load();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (i == count) break;
-                    go = go && __all_sync(0xffffffffu, mbar_wait_polls(at(&s.empty[c.slot]), c.parity ^ 1u));
+                for (int i = 0; i < kScaleRun; ++i) {
+                    if (i >= count) break;
+                    go = __all_sync(0xffffffffu, mbar_wait_polls(at(&s.empty[r.slot]), r.parity ^ 1u));
                     if (!go) break;
-                    const uint32_t to = tiles_at + c.slot * Layout::kStageBytes + Layout::kScales + lane * 16;
+                    const uint32_t to = tiles_at + r.slot * Layout::kStageBytes + Layout::kScales + group * kScaleTile +
+                                        lane * 16 + half * 8;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int g = 0; g < Layout::kGroups; ++g)
-                            st_shared_v4(to + (j * Layout::kGroups + g) * kScaleTile,
-                                         make_uint4(word_of(v[g][0], i * 2 + j), word_of(v[g][1], i * 2 + j),
-                                                    word_of(v[g][2], i * 2 + j), word_of(v[g][3], i * 2 + j)));
+                    for (int j = 0; j < 2; ++j)   // the stage's first and second 128 channels
+                        st_shared_v2(to + j * Layout::kGroups * kScaleTile, word_of(v[0][i / 2], i % 2 * 2 + j),
+                                     word_of(v[1][i / 2], i % 2 * 2 + j));
                     fence_proxy_async_smem();   // the copies to tensor memory read them
                     __syncwarp();
-                    if (kCtas == 2) mbar_release_cluster(full0 + c.slot * 8, issue);
-                    else mbar_arrive(at(&s.full[c.slot]), issue);
-                    c.advance(Layout::kStages);
+                    if (kCtas == 2) {
+                        fence_release_shared_cluster();
+                        mbar_arrive_cluster(full0 + r.slot * 8, issue);
+                    } else {
+                        mbar_arrive(at(&s.full[r.slot]), issue);
+                    }
+                    r.advance(Layout::kStages);
                 }
-                step();
-                if (t < total) step();
-                if (t < total) load();
+                count = after;
             }
         }
         if (kSplit) {   // the sums' exchange below
@@ -397,8 +416,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + wg * kFirst;
         const uint32_t first_empty = kCtas == 2 ? first_block_address(at(&s.acc_empty[0])) : 0;   // 8 bytes each
         Ring acc;
+        Mx4Tile tile = {};
         for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += stride) {
-            const Mx4Tile tile = mx4_tile<kCtas>(s, p, t, rank);
+            mx4_go<kCtas>(tile, s, p, t, rank);
             float2 v[kHalves * 32];
             {
                 uint32_t r[kHalves * 4][16];
@@ -576,7 +596,7 @@ static cudaError_t launch_mx4_tiles(const void *a, const void *w, Mx4Args p, cud
     cudaLaunchConfig_t cfg = {};
     const int parts = kSplit ? p.split : 1;
     cfg.gridDim = dim3((unsigned)(kSplit ? most * parts : kCtas * (most < groups ? (most > 0 ? most : 1) : groups)));
-    cfg.blockDim = dim3(kProductThreads);
+    cfg.blockDim = dim3(kMx4Threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -328,14 +328,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, bool issue) {
         : "memory");
 }
 
-// The same with release: what the thread wrote before is seen by who waits.
-__device__ __forceinline__ void mbar_release_cluster(uint32_t bar, bool issue) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
-        "r"((uint32_t)issue)
-        : "memory");
+// For such an arrival that does publish writes to this block's shared memory, and
+// for who waits for it: fences of that alone (a release of everything at cluster
+// scope takes the 900 cycles above).
+__device__ __forceinline__ void fence_release_shared_cluster() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void fence_acquire_shared_cluster() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -358,6 +358,9 @@ __device__ __forceinline__ void fence_mbarrier_init() {
 __device__ __forceinline__ void st_shared_v4(uint32_t p, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t p, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t p) {
     uint4 v;

@@ -257,16 +257,19 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                     const uint32_t bar = at(&s.full[r.slot]);
 #ifdef MOE_TEST_WITHHOLD_PRODUCT_STAGE
                     // Test builds only: the loads of this stage never happen, so the waits run out.
-                    const bool load = issue && issued != MOE_TEST_WITHHOLD_PRODUCT_STAGE;
+                    const bool load = elect_one() && issued != MOE_TEST_WITHHOLD_PRODUCT_STAGE;
 #else
-                    const bool load = issue;
+                    const bool load = elect_one();
 #endif
-                    mbar_expect(bar, bytes, load && rank == 0);
-                    tensor_load_2d<kCtas>(a, rows, kb * (kMx4K / 2), tile.row0, bar, load && tile.valid > 0);
+                    if (load) {
+                        if (rank == 0) mbar_expect(bar, bytes, true);
+                        if (tile.valid > 0) tensor_load_2d<kCtas>(a, rows, kb * (kMx4K / 2), tile.row0, bar, true);
 #pragma unroll
-                    for (int i = 0; i < kBoxes; ++i)
-                        tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, kb * (kMx4K / 2),
-                                              first + i * (kGated ? p.N / 2 : kBox), tile.e, bar, load);
+                        for (int i = 0; i < kBoxes; ++i)
+                            tensor_load_3d<kCtas>(w + i * kBoxBytes, &map_w, kb * (kMx4K / 2),
+                                                  first + i * (kGated ? p.N / 2 : kBox), tile.e, bar, true);
+                    }
+                    __syncwarp();
                     r.advance(Layout::kStages);
                     ++issued;
                 }
@@ -307,27 +310,33 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                         if (kCtas == 2) fence_acquire_shared_cluster();   // the other block's scales
                         tcgen05_fence_after();
                         const uint64_t step = (uint32_t)r.slot * (Layout::kStageBytes >> 4);
-                        // group g's scales of the stage's first and second 128 channels: columns
-                        // 4 g on of the first or second run of kGroups * 4
+                        if (elect_one()) {
+                            // group g's scales of the stage's first and second 128 channels: columns
+                            // 4 g on of the first or second run of kGroups * 4
 #pragma unroll
-                        for (int j = 0; j < 2 * Layout::kGroups; ++j)
-                            tmem_copy_scales<kCtas>(scales + j * 4, s0 + step + j * (kScaleTile >> 4), issue);
+                            for (int j = 0; j < 2 * Layout::kGroups; ++j)
+                                tmem_copy_scales<kCtas>(scales + j * 4, s0 + step + j * (kScaleTile >> 4), true);
 #pragma unroll
-                        for (int k = 0; k < kMx4K / 64; ++k) {
-                            const uint32_t from = scales + (k >> 1) * Layout::kGroups * 4;
-                            mma_mx4<kCtas>(d, a0 + step + k * 2, w0 + step + k * 2, instruction | mx4_scales((k & 1) * 2),
-                                           from, from + 4, kb > 0 || k > 0, issue);
+                            for (int k = 0; k < kMx4K / 64; ++k) {
+                                const uint32_t from = scales + (k >> 1) * Layout::kGroups * 4;
+                                mma_mx4<kCtas>(d, a0 + step + k * 2, w0 + step + k * 2,
+                                               instruction | mx4_scales((k & 1) * 2), from, from + 4, kb > 0 || k > 0,
+                                               true);
+                            }
+                            mma_commit<kCtas>(at(&s.empty[r.slot]), true);
                         }
-                        mma_commit<kCtas>(at(&s.empty[r.slot]), issue);
+                        __syncwarp();
                         r.advance(Layout::kStages);
                         go = __all_sync(0xffffffffu, full);
                         if (!go) break;
                     }
-                    mma_commit<kCtas>(at(&s.acc_full[acc.slot]), issue);
+                    if (elect_one()) mma_commit<kCtas>(at(&s.acc_full[acc.slot]), true);
+                    __syncwarp();
                     acc.advance(2);
                 }
                 if (!go) {   // leave no product running
-                    mma_commit<kCtas>(at(&s.drain), issue);
+                    if (elect_one()) mma_commit<kCtas>(at(&s.drain), true);
+                    __syncwarp();
                     mbar_wait_polls(at(&s.drain), 0);
                 }
             }

@@ -23,7 +23,8 @@ _API = {
     "rms_norm", "rms_norm_backward", "rms_norm_workspace_bytes", "NormResult", "NormGrad",
 }
 
-_LAYER = {"expert_layer", "expert_layer_backward", "ExpertWeights", "ExpertForward", "quantize_blocks"}
+_LAYER = {"expert_layer", "expert_layer_backward", "ExpertWeights", "ExpertForward", "quantize_blocks",
+          "ExpertWeightsMx4", "expert_block", "expert_block_backward", "BlockForward", "BlockGrad"}
 
 __all__ = sorted(_API) + sorted(_LAYER) + ["workloads", "HostLayerPipeline"]
 

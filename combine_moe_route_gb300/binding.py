@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -747,6 +748,17 @@ def _on(t: torch.Tensor, *others: torch.Tensor | None) -> None:
             raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
 
 
+def _all_fine(index: int, *expected) -> bool:
+    """Whether every (tensor or None, dtype, shape) is a contiguous tensor of that type and shape on
+    device ``index``: the whole check of a call that is in order, in a third of the time.  Where it is
+    not, ``_dev`` and ``_on`` say what is wrong."""
+    for t, dtype, shape in expected:
+        if t is not None and not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+                                  and t.get_device() == index and t.is_contiguous()):
+            return False
+    return index >= 0
+
+
 # the current stream's handle without a Stream object (2 us of a small call's 14)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -895,6 +907,12 @@ def dequantize_mx4(q: torch.Tensor, scale: torch.Tensor | None, *, out: torch.Te
 
 
 def _mx4_operands(a, a_scale, w, w_scale, expert_offsets):
+    if type(a) is torch.Tensor and type(w) is torch.Tensor and a.dim() == 2 and w.dim() == 3:
+        (rows, half), (E, N, _) = a.shape, w.shape   # the common call, all in order
+        if not half % 16 and _all_fine(a.get_device(), (a, torch.uint8, (rows, half)),
+                                       (a_scale, torch.uint8, (rows, half // 16)), (w, torch.uint8, (E, N, half)),
+                                       (w_scale, torch.uint8, (E, N, half // 16)), (expert_offsets, torch.int32, (E + 1,))):
+            return rows, E, N, 2 * half
     _dev(a, "a", _CODES)
     _dev(w, "w", _CODES)
     if a.dim() != 2 or w.dim() != 3:
@@ -1099,35 +1117,40 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | 
     _dev(x, "x", torch.bfloat16)
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    _dev(weight, "weight", torch.bfloat16, (H,))
+    shape = x.shape
+    T, H = shape
     if not eps >= 0.0:
         raise ValueError("eps must not be negative")
     if fp8 and H % 128:
         raise ValueError("fp8 needs H a multiple of 128")
-    dev = x.device
+    dev, bf16 = x.device, torch.bfloat16
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    _dev(out, "out", torch.bfloat16, (T, H))
-    if residual is not None:
-        _dev(residual, "residual", torch.bfloat16, (T, H))
-        if out_h is None:
-            out_h = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-        _dev(out_h, "out_h", torch.bfloat16, (T, H))
-        if out_h.data_ptr() == out.data_ptr() and T:
-            raise ValueError("out and out_h must be two buffers")
-    else:
+        out = torch.empty(shape, dtype=bf16, device=dev)
+    if residual is None:
         out_h = None
-    if fp8:
+    elif out_h is None:
+        out_h = torch.empty(shape, dtype=bf16, device=dev)
+    if not fp8:
+        out_q = out_scale = None
+    else:
         if out_q is None:
-            out_q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
+            out_q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
         if out_scale is None:
             out_scale = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
-        _dev(out_q, "out_q", _E4M3, (T, H))
-        _dev(out_scale, "out_scale", torch.float32, (T, H // 128))
-    else:
-        out_q = out_scale = None
-    _on(x, weight, residual, out, out_h, out_q, out_scale)
+    if not _all_fine(x.get_device(), (weight, bf16, (H,)), (residual, bf16, shape), (out, bf16, shape),
+                     (out_h, bf16, shape), (out_q, torch.float8_e4m3fn, shape),
+                     (out_scale, torch.float32, (T, H // 128))):
+        _dev(weight, "weight", bf16, (H,))
+        _dev(out, "out", bf16, shape)
+        if residual is not None:
+            _dev(residual, "residual", bf16, shape)
+            _dev(out_h, "out_h", bf16, shape)
+        if fp8:
+            _dev(out_q, "out_q", _E4M3, shape)
+            _dev(out_scale, "out_scale", torch.float32, (T, H // 128))
+        _on(x, weight, residual, out, out_h, out_q, out_scale)
+    if out_h is not None and T and out_h.data_ptr() == out.data_ptr():
+        raise ValueError("out and out_h must be two buffers")
     _enqueue("moe_rms_norm", x, stream, x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, eps, out.data_ptr(),
              _ptr(out_h), _ptr(out_q), _ptr(out_scale))
     return NormResult(out, x if residual is None else out_h, out_q, out_scale)
@@ -1149,30 +1172,41 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, *
     _dev(h, "h", torch.bfloat16)
     if h.dim() != 2:
         raise ValueError("h must be [T, H]")
-    T, H = h.shape
-    _dev(dy, "dy", torch.bfloat16, (T, H))
-    _dev(weight, "weight", torch.bfloat16, (H,))
-    if dh is not None:
-        _dev(dh, "dh", torch.bfloat16, (T, H))
+    shape = h.shape
+    T, H = shape
     if not eps >= 0.0:
         raise ValueError("eps must not be negative")
-    dev = h.device
+    dev, bf16 = h.device, torch.bfloat16
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=bf16, device=dev)
     if dweight is None:
         dweight = torch.empty(H, dtype=torch.float32, device=dev)
-    _dev(out, "out", torch.bfloat16, (T, H))
-    _dev(dweight, "dweight", torch.float32, (H,))
     if workspace is None:
-        workspace = torch.empty(max(rms_norm_workspace_bytes(T, H), 16), dtype=torch.uint8, device=dev)
-        if stream is not None:   # dropped here, while the stream has yet to use it
-            workspace.record_stream(stream)
-    _dev(workspace, "workspace", torch.uint8)
-    _on(h, dy, weight, dh, out, dweight, workspace)
+        need = rms_norm_workspace_bytes(T, H)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            if stream is not None:   # dropped here, while the stream has yet to use it
+                workspace.record_stream(stream)
+    if not _all_fine(h.get_device(), (dy, bf16, shape), (weight, bf16, (H,)), (dh, bf16, shape), (out, bf16, shape),
+                     (dweight, torch.float32, (H,))):
+        _dev(dy, "dy", bf16, shape)
+        _dev(weight, "weight", bf16, (H,))
+        if dh is not None:
+            _dev(dh, "dh", bf16, shape)
+        _dev(out, "out", bf16, shape)
+        _dev(dweight, "dweight", torch.float32, (H,))
+        _on(h, dy, weight, dh, out, dweight)
+    size = 0
+    if workspace is not None:
+        _dev(workspace, "workspace", torch.uint8)
+        _on(h, workspace)
+        size = workspace.numel()
     _enqueue("moe_rms_norm_backward", h, stream, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _ptr(dh), T, H, eps,
-             out.data_ptr(), dweight.data_ptr(), workspace.data_ptr(), workspace.numel())
+             out.data_ptr(), dweight.data_ptr(), _ptr(workspace), size)
     return NormGrad(out, dweight)
 
 
+@functools.lru_cache(maxsize=256)
 def rms_norm_workspace_bytes(T: int, H: int) -> int:
+    """Bytes of workspace that ``rms_norm_backward`` needs, 0 for few short rows."""
     return int(load_library().moe_rms_norm_workspace_bytes(T, H))

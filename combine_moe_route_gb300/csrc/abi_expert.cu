@@ -122,7 +122,8 @@ moe_status moe_rms_norm_backward(const void *dy, const void *h, const void *weig
                                  moe_stream_t stream) {
     if (T < 0 || !hidden_ok(H) || !(eps >= 0.0f) || !dweight) return MOE_ERR_INVALID_ARG;
     if (T > 0 && (!dy || !h || !weight || !dx)) return MOE_ERR_INVALID_ARG;
-    if (T > 0 && (!workspace || workspace_bytes < moe::norm_workspace_bytes(T, H))) return MOE_ERR_WORKSPACE;
+    const size_t need = moe_rms_norm_workspace_bytes(T, H);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
     if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(dh) || !aligned16(dx) ||
         !aligned16(workspace))
         return MOE_ERR_UNSUPPORTED;

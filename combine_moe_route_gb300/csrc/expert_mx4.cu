@@ -107,16 +107,21 @@ struct Mx4Tile {
     int pair_valid;          // rows of the blocks together
 };
 
-template <int kCtas, class Shared>
-__device__ __forceinline__ void mx4_go(Mx4Tile &w, const Shared &s, const Mx4Args &p, long long t, int rank) {
+template <class Shared>
+__device__ __forceinline__ void mx4_seek(Mx4Tile &w, const Shared &s, const Mx4Args &p, long long t) {
     w.t = t;
-    if (t >= w.end) {
-        w.e = upper_bound_minus_one(s.tiles, p.E, (int)(t / p.ntiles));
-        w.mt = s.tiles[w.e + 1] - s.tiles[w.e];
-        w.begin = (long long)s.tiles[w.e] * p.ntiles;
-        w.end = w.begin + (long long)w.mt * p.ntiles;
-        w.rows = expert_rows(p, w.e);
-    }
+    if (t < w.end) return;
+    const int row_tile = (t >> 32) == 0 ? (int)((uint32_t)t / (uint32_t)p.ntiles) : (int)(t / p.ntiles);
+    w.e = upper_bound_minus_one(s.tiles, p.E, row_tile);
+    w.mt = s.tiles[w.e + 1] - s.tiles[w.e];
+    w.begin = (long long)s.tiles[w.e] * p.ntiles;
+    w.end = w.begin + (long long)w.mt * p.ntiles;
+    w.rows = expert_rows(p, w.e);   // in flight until mx4_place
+}
+
+template <int kCtas>
+__device__ __forceinline__ void mx4_place(Mx4Tile &w, const Mx4Args &p, int rank) {
+    const long long t = w.t;
     const uint32_t i = (uint32_t)(t - w.begin);   // an expert's tiles: under 2^32 (2^24 row tiles of 2^8 column tiles)
     w.n = (int)(i / (uint32_t)w.mt);
     const int m = kCtas == 1 && p.tails ? w.rows.y / (2 * kRowTile) * 2
@@ -124,6 +129,12 @@ __device__ __forceinline__ void mx4_go(Mx4Tile &w, const Shared &s, const Mx4Arg
     w.pair_valid = min(w.rows.y - m * kRowTile, kCtas * kRowTile);
     w.row0 = w.rows.x + (m + rank) * kRowTile;
     w.valid = max(min(w.pair_valid - rank * kRowTile, kRowTile), 0);
+}
+
+template <int kCtas, class Shared>
+__device__ __forceinline__ void mx4_go(Mx4Tile &w, const Shared &s, const Mx4Args &p, long long t, int rank) {
+    mx4_seek(w, s, p, t);
+    mx4_place<kCtas>(w, p, rank);
 }
 
 // 16 scales of a row, those past its end as 0 (their channels are 0 too).
@@ -426,8 +437,10 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         const uint32_t first_empty = kCtas == 2 ? first_block_address(at(&s.acc_empty[0])) : 0;   // 8 bytes each
         Ring acc;
         Mx4Tile tile = {};
-        for (long long t = blockIdx.x / (kCtas * parts); go && t < total; t += stride) {
-            mx4_go<kCtas>(tile, s, p, t, rank);
+        long long t = blockIdx.x / (kCtas * parts);
+        if (t < total) mx4_seek(tile, s, p, t);
+        while (go && t < total) {
+            mx4_place<kCtas>(tile, p, rank);
             float2 v[kHalves * 32];
             {
                 uint32_t r[kHalves * 4][16];
@@ -519,6 +532,8 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
             if (!go) break;
             const int n0 = tile.n * kTileColumns + wg * kFirst;                // first column
             const size_t warp_row = (size_t)tile.row0 + quarter * 32;
+            t += stride;   // the next tile's rows come while this one is written
+            if (t < total) mx4_seek(tile, s, p, t);
             if constexpr (kGated) {
                 const int I = p.N / 2;
                 const size_t row = warp_row + lane;
@@ -638,14 +653,16 @@ static cudaError_t launch_mx4(const void *a, const void *w, Mx4Args p, cudaStrea
         return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
     };
     p.a_width = width(p.a_scale), p.w_width = width(p.w_scale);
-#ifndef NO_PAIRS
-    if (p.rows > (long long)p.E * kRowTile) {
+    // Pairs where experts have so many rows that the rests, whose launch reads the weight again,
+    // weigh little.  Single blocks and pairs, 7168 x 2048: 256 experts x 1024 rows 1705 and 1650
+    // us, 128 x 600 537 and 592, 128 x 400 466 and 406, 256 x 256 580 and 623; gated, 2 x 2048 x
+    // 7168: 256 x 1024 2800 and 2730, 128 x 600 877 and 963, 128 x 400 671 and 648.
+    if (p.rows > (long long)p.E * 6 * kRowTile) {
         e = launch_mx4_tiles<2, 256, kGated>(a, w, p, stream);
         if (e != cudaSuccess) return e;
         p.tails = true;
         return launch_mx4_tiles<1, 256, kGated>(a, w, p, stream);
     }
-#endif
     const long long row_tiles = (long long)p.rows / kRowTile + (p.rows < p.E ? p.rows : p.E);   // at most
     constexpr int kNarrow = kGated ? 256 : 128;
     p.split = mx4_split_parts(row_tiles * ((p.N + kNarrow - 1) / kNarrow), p.C);

@@ -9,7 +9,15 @@ from the combine's.  The weights are quantised parameters and get no gradient; t
 pass gradients through unchanged.  Autograd records neither pass: a tensor that requires a gradient
 gets none through ``expert_layer``, only from ``expert_layer_backward``.
 
-``python -m combine_moe_route_gb300.experts`` runs one layer both ways on the GPU.
+With ``ExpertWeightsMx4`` the experts are 4-bit (e2m1 values, a power-of-two scale per 32 channels):
+route -> bf16 dispatch -> quantisation of its rows -> gated first product (quantised by its own
+epilogue) -> second product -> combine.  That is a serving form without a gradient.
+
+``expert_block`` puts in front of the layer what a transformer block has there: the residual's
+addition, the root-mean-square norm and the router's product.
+
+``python -m combine_moe_route_gb300.experts`` runs a layer and a block both ways on the GPU, and the
+block with 4-bit experts.
 """
 from __future__ import annotations
 
@@ -45,6 +53,25 @@ class ExpertWeights:
     @classmethod
     def quantized(cls, w13: torch.Tensor, w2: torch.Tensor) -> "ExpertWeights":
         return cls(*quantize_blocks(w13), *quantize_blocks(w2))
+
+    @property
+    def E(self) -> int:
+        return self.w13.shape[0]
+
+
+@dataclass
+class ExpertWeightsMx4:
+    """The experts of a layer in 4 bits: codes w13 [E, 2I, H/2] (each gate's I rows, then its up
+    projection's) and w2 [E, H, I/2], with a scale byte per 32 channels."""
+    w13: torch.Tensor
+    w13_scale: torch.Tensor
+    w2: torch.Tensor
+    w2_scale: torch.Tensor
+
+    @classmethod
+    def quantized(cls, w13: torch.Tensor, w2: torch.Tensor) -> "ExpertWeightsMx4":
+        """From bf16 or fp32 weights [E, 2I, H] and [E, H, I] on the GPU, once, when they are loaded."""
+        return cls(*_b.quantize_mx4(w13), *_b.quantize_mx4(w2))
 
     @property
     def E(self) -> int:
@@ -88,19 +115,28 @@ def _on(stream, inputs: tuple, run):
     return result
 
 
-def expert_layer(x: torch.Tensor, logits: torch.Tensor, B, K: int, weights: ExpertWeights, *, train: bool = False,
-                 out_dtype: torch.dtype = torch.bfloat16, stream=None) -> ExpertForward:
+def expert_layer(x: torch.Tensor, logits: torch.Tensor, B, K: int, weights: ExpertWeights | ExpertWeightsMx4, *,
+                 train: bool = False, out_dtype: torch.dtype = torch.bfloat16, stream=None) -> ExpertForward:
     """One layer: x [T, H] bf16 and logits [T, E] fp32 to the combined [T, H].  ``train`` keeps the
-    pre-activations for ``expert_layer_backward``.  Everything is enqueued on ``stream`` (default: the
+    pre-activations for ``expert_layer_backward`` (e4m3 weights only).  Everything is enqueued on ``stream`` (default: the
     current one), nothing synchronises: a given stream has to be ordered behind the work that writes
     the inputs, and whoever reads the results behind the stream."""
     E = weights.E
     if len(logits.shape) != 2 or logits.shape[1] != E:
         raise ValueError(f"logits must be [T, E] with a column for each of the weights' {E} experts, got "
                          f"{tuple(logits.shape)}")
+    mx4 = isinstance(weights, ExpertWeightsMx4)
+    if mx4 and train:
+        raise ValueError("4-bit experts have no gradient: train needs ExpertWeights")
 
     def run():
         idx, w = _b.route_topk(logits, K)
+        if mx4:
+            d = _b.dispatch(x, idx, B, E)
+            q, scale = _b.quantize_mx4(d.recv_x)
+            g = _b.expert_gated_gemm_mx4(q, scale, weights.w13, weights.w13_scale, d.expert_offsets)
+            y = _b.expert_gemm_mx4(g.q, g.scale, weights.w2, weights.w2_scale, d.expert_offsets)
+            return ExpertForward(_b.combine(y, d.tok2row, w, out_dtype=out_dtype), idx, w, d, g, y)
         d = _b.dispatch(x, idx, B, E, fp8=True)
         g = _b.expert_gated_gemm(d.recv_x, d.recv_scale, weights.w13, weights.w13_scale, d.expert_offsets,
                                  save_h=train)
@@ -128,6 +164,52 @@ def expert_layer_backward(dout: torch.Tensor, fwd: ExpertForward, weights: Exper
     return _on(stream, (dout, fwd, weights), run)
 
 
+@dataclass
+class BlockForward:
+    out: torch.Tensor                   # [T, H] bf16: the layer's output, the next block's x
+    h: torch.Tensor                     # [T, H] bf16: x + residual, the next block's residual
+    y: torch.Tensor                     # [T, H] bf16: the normed rows
+    logits: torch.Tensor                # [T, E] fp32
+    layer: ExpertForward
+    eps: float
+
+
+@dataclass
+class BlockGrad:
+    dx: torch.Tensor                    # [T, H] bf16: gradient of x, and of the residual
+    dnorm: torch.Tensor                 # [H] fp32
+    drouter: torch.Tensor               # [E, H] fp32
+
+
+def expert_block(x: torch.Tensor, residual: torch.Tensor | None, norm: torch.Tensor, router: torch.Tensor, B, K: int,
+                 weights: ExpertWeights | ExpertWeightsMx4, *, eps: float = 1e-6, train: bool = False,
+                 stream=None) -> BlockForward:
+    """h = x + residual, y = rms_norm(h) * norm, logits = y router^T (fp32), out = expert_layer(y, logits):
+    x and residual [T, H] bf16 (residual None in front of the first block), norm [H] bf16, router [E, H].
+    ``train`` and ``stream`` as ``expert_layer``."""
+    def run():
+        n = _b.rms_norm(x, norm, residual=residual, eps=eps)
+        logits = n.y.float() @ router.float().T
+        layer = expert_layer(n.y, logits, B, K, weights, train=train)
+        return BlockForward(layer.out, n.h, n.y, logits, layer, eps)
+
+    return _on(stream, (x, residual, norm, router, weights), run)
+
+
+def expert_block_backward(dout: torch.Tensor, dh: torch.Tensor | None, fwd: BlockForward, norm: torch.Tensor,
+                          router: torch.Tensor, weights: ExpertWeights, *, stream=None) -> BlockGrad:
+    """The block's gradient from those of its output (dout) and of its h (dh; None: nothing else uses
+    it), both [T, H] bf16, and a ``train`` forward."""
+    def run():
+        dy, dlogits = expert_layer_backward(dout, fwd.layer, weights)
+        drouter = dlogits.T @ fwd.y.float()
+        dy = torch.addmm(dy.float(), dlogits, router.float()).bfloat16()
+        g = _b.rms_norm_backward(dy, fwd.h, norm, dh=dh, eps=fwd.eps)
+        return BlockGrad(g.dx, g.dweight, drouter)
+
+    return _on(stream, (dout, dh, fwd, norm, router, weights), run)
+
+
 def main() -> None:
     T, H, inner, E, K, R = 512, 1024, 512, 32, 4, 8
     gen = torch.Generator(device="cuda").manual_seed(0)
@@ -139,10 +221,18 @@ def main() -> None:
     B = [T // R] * R
     fwd = expert_layer(x, logits, B, K, weights, train=True)
     dx, dlogits = expert_layer_backward(torch.ones_like(fwd.out), fwd, weights)
+    norm = torch.ones(H, device="cuda", dtype=torch.bfloat16)
+    router = torch.randn((E, H), generator=gen, device="cuda") / H ** 0.5
+    block = expert_block(fwd.out, x, norm, router, B, K, weights, train=True)
+    grad = expert_block_backward(torch.ones_like(fwd.out), torch.ones_like(fwd.out), block, norm, router, weights)
+    four = expert_block(fwd.out, x, norm, router, B, K, ExpertWeightsMx4.quantized(w13, w2))
     status, _ = _b.get_device_error(fwd.dispatch.workspace)
     print(f"{T} tokens, {E} experts, top-{K}: out {tuple(fwd.out.shape)} rms {fwd.out.float().square().mean().sqrt():.3f}, "
           f"dx rms {dx.float().square().mean().sqrt():.3f}, dlogits rms {dlogits.square().mean().sqrt():.4f}; "
           f"device status {status}, {_b.get_expert_error()[0]}")
+    off = (four.out.float() - block.out.float()).norm() / block.out.float().norm()
+    print(f"block: out rms {block.out.float().square().mean().sqrt():.3f}, dx rms {grad.dx.float().square().mean().sqrt():.3f}; "
+          f"4-bit experts are {off:.3f} of its norm away")
 
 
 if __name__ == "__main__":

@@ -615,7 +615,7 @@ MOE_API moe_status moe_expert_gated_gemm_mx4(const void *a, const void *a_scale,
 /*
  * moe_get_expert_error -- SYNCHRONOUS: waits for `stream`, then takes (reads and
  * clears in one step) the current device's error word of the four products above
- * into *host_code: MOE_DEVERR_COPY_TIMEOUT once a bounded wait inside one of
+ * and of moe_rms_norm_backward into *host_code: MOE_DEVERR_COPY_TIMEOUT once a bounded wait inside one of
  * their kernels has run out (the kernel then returns with its output
  * unspecified), else 0.  Returns MOE_ERR_TIMEOUT, or MOE_OK (MOE_ERR_CUDA with
  * *host_code 0 if the copy fails, as on a stream that is being captured,
@@ -723,7 +723,7 @@ MOE_API moe_status moe_dispatch_backward(const void *drows, const int32_t *tok2r
 MOE_API moe_status moe_rms_norm(const void *x, const void *residual, const void *weight, int T, int H, float eps,
                                 void *y, void *h, void *q, float *q_scale, moe_stream_t stream);
 
-/* Bytes of workspace moe_rms_norm_backward needs (0 for T < 1 or a bad H). */
+/* Bytes of workspace moe_rms_norm_backward needs (0 for T < 1 or a bad H, and for few short rows). */
 MOE_API size_t moe_rms_norm_workspace_bytes(int T, int H);
 
 /*
@@ -742,9 +742,9 @@ MOE_API size_t moe_rms_norm_workspace_bytes(int T, int H);
  *   dx         device bf16 [T, H], 16-byte aligned: out; may be dy, h or dh.
  *   dweight    device fp32 [H]: out (0 for T = 0).
  *   workspace  device, 16-byte aligned, moe_rms_norm_workspace_bytes(T, H) bytes,
- *              this call's alone until it is done (NULL for T = 0).
+ *              this call's alone until it is done (NULL where that is 0).
  * Errors: MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED / MOE_ERR_WORKSPACE /
- * MOE_ERR_CUDA.
+ * MOE_ERR_CUDA; a bounded wait that ran out is moe_get_expert_error's.
  */
 MOE_API moe_status moe_rms_norm_backward(const void *dy, const void *h, const void *weight, const void *dh, int T,
                                          int H, float eps, void *dx, float *dweight, void *workspace,

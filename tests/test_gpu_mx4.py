@@ -153,6 +153,20 @@ def test_scales_at_every_alignment(gpu, shift, C):
     assert torch.equal(b.expert_gemm_mx4(a, sa, w, moved(sw), off), want)
 
 
+@pytest.mark.parametrize("rows", [[1], [200, 33]])
+def test_result_at_16_bytes(gpu, rows):
+    """A result that starts between two 32-byte sectors, whole and in parts."""
+    from combine_moe_route_gb300 import binding as b
+    inp = ref.product_inputs(rows, 272, 2048, np.random.default_rng(9))
+    args = _to(gpu, inp)
+    want = b.expert_gemm_mx4(*args)
+    R = want.shape[0]
+    room = torch.full((R * 272 + 64,), 7.0, dtype=torch.bfloat16, device=gpu)
+    out = room[8:8 + R * 272].view(R, 272)
+    b.expert_gemm_mx4(*args, out=out)
+    assert torch.equal(out, want) and (room[:8] == 7).all() and (room[8 + R * 272:] == 7).all()
+
+
 def test_rows_stand_alone(gpu):
     """A NaN scale reaches its own row (or column) and nothing else; rows of no expert stay."""
     from combine_moe_route_gb300 import binding as b

@@ -84,8 +84,10 @@ def test_norm_backward(lib):
     for bad in (dict(T=-1), dict(H=4), dict(H=12), dict(H=16392), dict(eps=-1.0), dict(dy=None), dict(h=None),
                 dict(w=None), dict(dx=None), dict(dw=None)):
         assert call(**bad) == INVALID, bad
-    need = lib.moe_rms_norm_workspace_bytes(4, 256)
-    assert need >= 256 * 4 and call(n=need - 1) == WORKSPACE and call(ws=None) == WORKSPACE
+    need = lib.moe_rms_norm_workspace_bytes(4000, 2048)
+    assert need >= 2048 * 4
+    assert call(T=4000, H=2048, n=need - 1) == WORKSPACE and call(T=4000, H=2048, ws=None) == WORKSPACE
+    assert lib.moe_rms_norm_workspace_bytes(4, 256) == 0
     for odd in ("dy", "h", "w", "dh", "dx", "ws"):
         assert call(**{odd: ODD}) == UNSUPPORTED
     assert lib.moe_rms_norm_workspace_bytes(0, 256) == 0 == lib.moe_rms_norm_workspace_bytes(4, 20)

@@ -119,6 +119,108 @@ def test_long_contraction(gpu, counts, C):
             assert torch.equal(b.expert_gemm_mx4(*args, out_dtype=torch.float32), o)
 
 
+MANY = {"pairs": [1600], "pairs_and_rests": [2000, 5, 300, 1100], "half_a_pair": [900, 770], "blocks": [700, 690, 710]}
+
+
+@pytest.mark.parametrize("N,C", [(208, 160), (400, 640), (1328, 2048), (4096, 2880)])
+@pytest.mark.parametrize("name", sorted(MANY))
+def test_many_rows(gpu, name, N, C):
+    """Pairs of blocks with and without a rest, blocks of several tiles, rings that wrap often."""
+    from combine_moe_route_gb300 import binding as b
+    inp = ref.product_inputs(MANY[name], N, C, np.random.default_rng(N + C))
+    args = _to(gpu, inp)
+    w64, a64 = ref.values(inp["w"], inp["w_scale"]), ref.values(inp["a"], inp["a_scale"])
+    off = inp["off"].tolist()
+    o32 = b.expert_gemm_mx4(*args, out_dtype=torch.float32)
+    o16 = b.expert_gemm_mx4(*args)
+    assert torch.equal(o16, o32.bfloat16())
+    assert torch.equal(b.expert_gemm_mx4(*args, out_dtype=torch.float32), o32)
+    for e in range(len(MANY[name])):
+        rows = slice(off[e], off[e + 1])
+        want, mag = a64[rows] @ w64[e].T, a64[rows].abs() @ w64[e].abs().T
+        assert ((o32[rows].cpu().double() - want).abs() <= ref.product_bound(mag, C)).all()
+    assert b.get_expert_error()[0] == 0
+
+
+@pytest.mark.parametrize("I,C", [(96, 160), (256, 2048), (1024, 2880)])
+@pytest.mark.parametrize("name", sorted(MANY))
+def test_gated_many_rows(gpu, name, I, C):
+    from combine_moe_route_gb300 import binding as b
+    inp = ref.product_inputs(MANY[name], 2 * I, C, np.random.default_rng(I + C), spread=1)
+    inp["w_scale"] -= 5
+    p, mag = ref.product(inp)
+    err = ref.product_bound(mag, C)
+    g, u, eg, eu = p[:, :I], p[:, I:], err[:, :I], err[:, I:]
+    v = eref.gate(g, u)
+    bound = 1.1 * eg * (u.abs() + eu) + (g.abs() + eg) * eu + 16 * 2.0 ** -24 * v.abs()
+    r = b.expert_gated_gemm_mx4(*_to(gpu, inp))
+    assert ref.quantized_ok(r.q.cpu(), r.scale.cpu(), v, bound) == (True, True)
+
+
+def test_result_past_32_bits(gpu):
+    """70000 x 32768 values: the last rows' places are past 2^31 elements."""
+    from combine_moe_route_gb300 import binding as b
+    gen = torch.Generator(device=gpu).manual_seed(7)
+    R, N, C = 70000, 32768, 64
+    a, sa = b.quantize_mx4(torch.randn((R, C), generator=gen, device=gpu))
+    w, sw = b.quantize_mx4(torch.randn((1, N, C), generator=gen, device=gpu))
+    out = b.expert_gemm_mx4(a, sa, w, sw, torch.tensor([0, R], dtype=torch.int32, device=gpu))
+    for rows in (slice(0, 3), slice(65530, 65545), slice(R - 70, R)):
+        n = rows.stop - rows.start
+        small = b.expert_gemm_mx4(a[rows].clone(), sa[rows].clone(), w, sw, torch.tensor([0, n], dtype=torch.int32, device=gpu))
+        want = b.dequantize_mx4(a[rows].clone(), sa[rows].clone()).float() @ b.dequantize_mx4(w, sw)[0].float().T
+        assert torch.equal(out[rows], small) and (out[rows].float() - want).abs().max() <= 2.0 ** -8 * want.abs().max()
+
+
+def test_two_streams_at_once(gpu):
+    from combine_moe_route_gb300 import binding as b
+    gen = torch.Generator(device=gpu).manual_seed(8)
+    streams, work = [torch.cuda.Stream() for _ in range(2)], []
+    for i, rows in enumerate((900, 40)):
+        a, sa = b.quantize_mx4(torch.randn((rows, 2048), generator=gen, device=gpu))
+        w, sw = b.quantize_mx4(torch.randn((2, 512, 2048), generator=gen, device=gpu))
+        off = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device=gpu)
+        work.append((a, sa, w, sw, off))
+    want = [b.expert_gemm_mx4(*x) for x in work]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(b.expert_gemm_mx4(*work[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_first_call_of_a_process_inside_a_capture(gpu):
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from combine_moe_route_gb300 import binding as b
+x = torch.ones((300, 512), device="cuda", dtype=torch.bfloat16)
+w = torch.ones((1, 256, 512), device="cuda", dtype=torch.bfloat16)
+g = torch.ones(512, device="cuda", dtype=torch.bfloat16)
+off = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    q, s = b.quantize_mx4(b.rms_norm(x, g).y)
+    wq, ws = b.quantize_mx4(w)
+    out = b.expert_gemm_mx4(q, s, wq, ws, off)
+    grad = b.rms_norm_backward(x.repeat(1, 4), x.repeat(1, 4), g.repeat(4))
+graph.replay()
+torch.cuda.synchronize()
+assert (out == 512).all(), out
+assert torch.isfinite(grad.dweight).all()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=110)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 @pytest.mark.parametrize("I,C", [(128, 256), (32, 32), (96, 160), (256, 640), (416, 288), (160, 2048), (128, 7168)])
 @pytest.mark.parametrize("name", sorted(COUNTS))
 def test_gated(gpu, name, I, C):

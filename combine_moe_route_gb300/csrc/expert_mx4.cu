@@ -62,10 +62,12 @@ struct Mx4Layout {
     static constexpr int kScales = kWeight + kBN / kCtas * kMx4K / 2;
     static constexpr int kGroups = 1 + kBN / 128;                       // of 128 rows of scales: A's and the weight's
     static constexpr int kStageBytes = kScales + kGroups * 2 * kScaleTile;
+    // A pair's ring leaves room to stage 128 bytes of a warp's rows, for tensor stores.
+    static constexpr int kStagingBytes = kCtas == 2 ? 2 * kStagingWarp : kStagingWarp;   // of a warp
     // of 227 KB: 4.5 KB for the barriers and the experts' tiles, the output's staging, alignment
-    static constexpr int kStages = (227 * 1024 - 4608 - 8 * kStagingWarp - 1024) / kStageBytes;
+    static constexpr int kStages = (227 * 1024 - 4608 - 8 * kStagingBytes - 1024) / kStageBytes;
     static constexpr int kStaging = kStages * kStageBytes;
-    static constexpr int kBytes = kStaging + 8 * kStagingWarp + 1024;
+    static constexpr int kBytes = kStaging + 8 * kStagingBytes + 1024;
     // Two accumulators in turn.  Of 256 columns they share 48, so that the scales have room:
     // the next tile starts when the last one's shared columns are read.
     static constexpr int kShared = kBN == 256 ? 48 : 0;
@@ -163,7 +165,8 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
 template <int kCtas, int kBN, bool kGated, bool kSplit>
 __global__ void __launch_bounds__(kMx4Threads, 1)
     expert_mx4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_few,
-                      const __grid_constant__ CUtensorMap map_w, const Mx4Args p) {
+                      const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out,
+                      const Mx4Args p) {
     using Layout = Mx4Layout<kCtas, kBN>;
     constexpr int kTileColumns = kGated ? kBN / 2 : kBN;   // of the result
     extern __shared__ unsigned char s_raw[];
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         constexpr int kApart = kGated ? 128 : 64;                    // from one group to the next
         constexpr int kFirst = kGated || kHalves == 1 ? 64 : 128;    // from one warpgroup's first to the other's
         const int wg = warp >> 2, quarter = warp & 3;
-        const uint32_t stage = tiles_at + Layout::kStaging + warp * kStagingWarp;
+        const uint32_t stage = tiles_at + Layout::kStaging + warp * Layout::kStagingBytes;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + wg * kFirst;
         const uint32_t first_empty = kCtas == 2 ? first_block_address(at(&s.acc_empty[0])) : 0;   // 8 bytes each
         Ring acc;
@@ -562,6 +565,33 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
                     const int n = n0 + h * 64;
+                    if (kCtas == 2 && !p.out_f32 && keep == 32) {
+                        // 32 rows x 64 columns as one tensor store, which leaves out columns past N
+                        uint4 x[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float2 *f = v + h * 32 + c * 4;
+                            x[c] = make_uint4(bf16_pair(f[0].x, f[0].y), bf16_pair(f[1].x, f[1].y),
+                                              bf16_pair(f[2].x, f[2].y), bf16_pair(f[3].x, f[3].y));
+                        }
+                        if (n >= p.N) continue;
+                        bulk_wait_read<0>();   // the last store has read the staging (its lane's)
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) st_shared_v4(stage + lane * 128 + ((c ^ (lane & 7)) * 16), x[c]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (elect_one()) {
+                            tensor_store_2d(&map_out, n, (int)warp_row, stage);
+                            bulk_commit();
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                    if (kCtas == 2) {
+                        bulk_wait_read<0>();
+                        __syncwarp();
+                    }
                     if (!p.out_f32) {
                         store_bf16x64<kSplit>(v + h * 32, stage,
                                               static_cast<unsigned char *>(p.out) + (warp_row * p.N + n) * 2,
@@ -584,6 +614,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                 }
             }
         }
+        if (kCtas == 2 && !kGated) bulk_wait_all();   // the stores are done, and their staging is read
         if (kSplit && blockIdx.x / parts >= total) {   // no tile: the exchange is the cluster's all the same
             cluster_barrier();
             cluster_barrier();
@@ -602,9 +633,12 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
 
 template <int kCtas, int kBN, bool kGated, bool kSplit = false>
 static cudaError_t launch_mx4_tiles(const void *a, const void *w, Mx4Args p, cudaStream_t stream) {
-    CUtensorMap map_a, map_few, map_w;
+    CUtensorMap map_a, map_few, map_w, map_out;
     if (!encode_bytes(&map_a, a, p.C / 2, p.rows, 0, kRowTile) || !encode_bytes(&map_few, a, p.C / 2, p.rows, 0, kFewRows) ||
         !encode_bytes(&map_w, w, p.C / 2, p.N, p.E, kGated ? 128 : kBN / kCtas))
+        return cudaErrorInvalidValue;
+    map_out = map_a;   // not used, but for
+    if (kCtas == 2 && !kGated && !p.out_f32 && !encode_bf16(&map_out, p.out, p.N, p.rows, 64, 32))
         return cudaErrorInvalidValue;
     auto kernel = expert_mx4_kernel<kCtas, kBN, kGated, kSplit>;
     constexpr int smem = Mx4Layout<kCtas, kBN>::kBytes;
@@ -631,7 +665,7 @@ static cudaError_t launch_mx4_tiles(const void *a, const void *w, Mx4Args p, cud
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_few, map_w, p);
+    return cudaLaunchKernelEx(&cfg, kernel, map_a, map_few, map_w, map_out, p);
 }
 
 // Into how many parts a tile's channels are split so that few tiles use the card:

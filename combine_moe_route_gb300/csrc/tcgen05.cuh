@@ -264,6 +264,14 @@ __device__ __forceinline__ void tensor_load_3d(uint32_t dst, const CUtensorMap *
             : "memory");
 }
 
+// From this block's shared memory, tracked by the bulk async-group mechanism; what
+// lies past the tensor's end is left out.
+__device__ __forceinline__ void tensor_store_2d(const CUtensorMap *map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(src)
+                 : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

@@ -62,8 +62,10 @@ struct Mx4Layout {
     static constexpr int kScales = kWeight + kBN / kCtas * kMx4K / 2;
     static constexpr int kGroups = 1 + kBN / 128;                       // of 128 rows of scales: A's and the weight's
     static constexpr int kStageBytes = kScales + kGroups * 2 * kScaleTile;
-    // A pair's ring leaves room to stage 128 bytes of a warp's rows, for tensor stores.
-    static constexpr int kStagingBytes = kCtas == 2 ? 2 * kStagingWarp : kStagingWarp;   // of a warp
+    // Columns of a tensor store of 32 rows: a pair's ring leaves room to stage 128 bytes of a
+    // warp's rows, a single block's 64.
+    static constexpr int kStoreColumns = kCtas == 2 ? 64 : 32;
+    static constexpr int kStagingBytes = 32 * kStoreColumns * 2;   // of a warp
     // of 227 KB: 4.5 KB for the barriers and the experts' tiles, the output's staging, alignment
     static constexpr int kStages = (227 * 1024 - 4608 - 8 * kStagingBytes - 1024) / kStageBytes;
     static constexpr int kStaging = kStages * kStageBytes;
@@ -565,30 +567,35 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
                     const int n = n0 + h * 64;
-                    if (kCtas == 2 && !p.out_f32 && keep == 32) {
-                        // 32 rows x 64 columns as one tensor store, which leaves out columns past N
-                        uint4 x[8];
+                    if (!kSplit && !p.out_f32 && keep == 32) {
+                        // 32 rows x kStoreColumns as one tensor store, which leaves out columns past N
+                        constexpr int kChunks = Layout::kStoreColumns / 8;   // of 16 bytes of a row
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float2 *f = v + h * 32 + c * 4;
-                            x[c] = make_uint4(bf16_pair(f[0].x, f[0].y), bf16_pair(f[1].x, f[1].y),
-                                              bf16_pair(f[2].x, f[2].y), bf16_pair(f[3].x, f[3].y));
-                        }
-                        if (n >= p.N) continue;
-                        bulk_wait_read<0>();   // the last store has read the staging (its lane's)
-                        __syncwarp();
+                        for (int part = 0; part < 8 / kChunks; ++part) {
+                            const int at_n = n + part * Layout::kStoreColumns;
+                            if (at_n >= p.N) break;
+                            bulk_wait_read<0>();   // the last store has read the staging
+                            __syncwarp();
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) st_shared_v4(stage + lane * 128 + ((c ^ (lane & 7)) * 16), x[c]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (elect_one()) {
-                            tensor_store_2d(&map_out, n, (int)warp_row, stage);
-                            bulk_commit();
+                            for (int c = 0; c < kChunks; ++c) {
+                                const float2 *f = v + h * 32 + (part * kChunks + c) * 4;
+                                // the swizzle of 128- or 64-byte rows
+                                const int to = kChunks == 8 ? c ^ (lane & 7) : c ^ ((lane >> 1) & 3);
+                                st_shared_v4(stage + lane * (kChunks * 16) + to * 16,
+                                             make_uint4(bf16_pair(f[0].x, f[0].y), bf16_pair(f[1].x, f[1].y),
+                                                        bf16_pair(f[2].x, f[2].y), bf16_pair(f[3].x, f[3].y)));
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (elect_one()) {
+                                tensor_store_2d(&map_out, at_n, (int)warp_row, stage);
+                                bulk_commit();
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                         continue;
                     }
-                    if (kCtas == 2) {
+                    if (!kSplit) {
                         bulk_wait_read<0>();
                         __syncwarp();
                     }
@@ -614,7 +621,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                 }
             }
         }
-        if (kCtas == 2 && !kGated) bulk_wait_all();   // the stores are done, and their staging is read
+        if (!kSplit && !kGated) bulk_wait_all();   // the stores are done, and their staging is read
         if (kSplit && blockIdx.x / parts >= total) {   // no tile: the exchange is the cluster's all the same
             cluster_barrier();
             cluster_barrier();
@@ -638,7 +645,8 @@ static cudaError_t launch_mx4_tiles(const void *a, const void *w, Mx4Args p, cud
         !encode_bytes(&map_w, w, p.C / 2, p.N, p.E, kGated ? 128 : kBN / kCtas))
         return cudaErrorInvalidValue;
     map_out = map_a;   // not used, but for
-    if (kCtas == 2 && !kGated && !p.out_f32 && !encode_bf16(&map_out, p.out, p.N, p.rows, 64, 32))
+    if (!kSplit && !kGated && !p.out_f32 &&
+        !encode_bf16(&map_out, p.out, p.N, p.rows, Mx4Layout<kCtas, kBN>::kStoreColumns, 32))
         return cudaErrorInvalidValue;
     auto kernel = expert_mx4_kernel<kCtas, kBN, kGated, kSplit>;
     constexpr int smem = Mx4Layout<kCtas, kBN>::kBytes;

@@ -116,14 +116,14 @@ inline bool encode_bytes(CUtensorMap *map, const void *base, uint64_t x, uint64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 matrix of y rows of x (dense), boxes of nx x ny (128 bytes wide), 128-byte swizzle.
+// bf16 matrix of y rows of x (dense), boxes of nx x ny, 64 or 128 bytes wide and swizzled as wide.
 inline bool encode_bf16(CUtensorMap *map, void *base, uint64_t x, uint64_t y, int nx, int ny) {
     const EncodeTiled f = encode_tiled();
     if (!f) return false;
     const cuuint64_t dims[2] = {x, y}, strides[1] = {2 * x};
     const cuuint32_t box[2] = {(cuuint32_t)nx, (cuuint32_t)ny}, elem[2] = {1, 1};
     return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             nx == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

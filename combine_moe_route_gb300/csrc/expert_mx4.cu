@@ -22,6 +22,12 @@
 //                quantise it: a block of 32 channels is one thread's.
 // Rows past a tile's own are the next expert's, or hold leftovers; nothing reads
 // them (a row of the result depends on its own row of A and its scales alone).
+//
+// What bounds it: few rows, the weight's bytes (384 experts of skewed load, 1003
+// tokens x top-8, 7168 x 2048: 0.85 GB in 143 us, 0.88 of the measured copy rate).
+// Many rows, a stage takes about 750 cycles, of which its products are 493 and its
+// loads about as many: 8 experts x 1024 rows, 2 x 2048 x 7168 gated in 93 us (5.2
+// PFLOP/s; products alone 62, loads alone 65), 7168 x 2048 in 58 us (4.1 PFLOP/s).
 #include <atomic>
 
 #include "launch.h"
@@ -676,13 +682,16 @@ static cudaError_t launch_mx4_tiles(const void *a, const void *w, Mx4Args p, cud
     return cudaLaunchKernelEx(&cfg, kernel, map_a, map_few, map_w, map_out, p);
 }
 
-// Into how many parts a tile's channels are split so that few tiles use the card:
-// at least four stages each, and no more clusters than fit at once.
+// Into how many parts a tile's channels are split so that few tiles use the card: at
+// least four stages each, and no more clusters than fit at once (of 152 SMs, 36 of
+// four, 76 of two).  8 rows an expert, L2 flushed before each call, in one, two and
+// four parts: gated, 1 expert x 2048 x 7168, 16 tiles, 21.2, 19.1 and 19.1 us (four are
+// taken); x 1024 x 7168, 8 tiles, 21.2, 19.0 and 17.1 (four); 2 experts x 2048 x 7168,
+// 32 tiles, 23.2, 21.2 and 21.2 (four); product, 2048 x 7168, 16 tiles, 15.0, 15.0 and 13.0.
 static int mx4_split_parts(long long tiles, int C) {
     const int stages = (C + kMx4K - 1) / kMx4K;
-    for (int parts = 8; parts > 1; parts /= 2)
-        if (tiles * parts <= device_sm_count() * (parts == 8 ? 0.79 : parts == 4 ? 0.95 : 1.0) && stages >= 4 * parts)
-            return parts;
+    for (int parts = 4; parts > 1; parts /= 2)
+        if (tiles * parts <= device_sm_count() * (parts == 4 ? 0.95 : 1.0) && stages >= 4 * parts) return parts;
     return 1;
 }
 
@@ -696,9 +705,9 @@ static cudaError_t launch_mx4(const void *a, const void *w, Mx4Args p, cudaStrea
     };
     p.a_width = width(p.a_scale), p.w_width = width(p.w_scale);
     // Pairs where experts have so many rows that the rests, whose launch reads the weight again,
-    // weigh little.  Single blocks and pairs, 7168 x 2048: 256 experts x 1024 rows 1705 and 1650
-    // us, 128 x 600 537 and 592, 128 x 400 466 and 406, 256 x 256 580 and 623; gated, 2 x 2048 x
-    // 7168: 256 x 1024 2800 and 2730, 128 x 600 877 and 963, 128 x 400 671 and 648.
+    // weigh little.  Single blocks and pairs, 7168 x 2048: 256 experts x 1024 rows 1547 and 1535
+    // us, 128 x 600 490 and 565; gated, 2 x 2048 x 7168: 256 x 1024 2780 to 2850 and 2710, 128 x
+    // 600 877 and 963 (128 x 400, where a pair's two tiles waste less, 668 and 640).
     if (p.rows > (long long)p.E * 6 * kRowTile) {
         e = launch_mx4_tiles<2, 256, kGated>(a, w, p, stream);
         if (e != cudaSuccess) return e;
@@ -710,7 +719,11 @@ static cudaError_t launch_mx4(const void *a, const void *w, Mx4Args p, cudaStrea
     p.split = mx4_split_parts(row_tiles * ((p.N + kNarrow - 1) / kNarrow), p.C);
     if (p.split > 1) return launch_mx4_tiles<1, kNarrow, kGated, true>(a, w, p, stream);
     if constexpr (!kGated) {
-        if (row_tiles * ((p.N + 255) / 256) < 4 * device_sm_count()) return launch_mx4_tiles<1, 128, kGated>(a, w, p, stream);
+        // where tiles are few, 128 columns spread over more SMs; else 256 read A half as often: 7168 x
+        // 2048, 8 rows an expert, 128 and 256 columns: 16 experts 33.4 and 35.5 us, 32 experts 58.0
+        // both, 64 experts 98.9 and 96.9
+        if (row_tiles * ((p.N + 255) / 256) < 4 * device_sm_count())
+            return launch_mx4_tiles<1, 128, kGated>(a, w, p, stream);
     }
     return launch_mx4_tiles<1, 256, kGated>(a, w, p, stream);
 }

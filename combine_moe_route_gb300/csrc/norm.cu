@@ -11,6 +11,10 @@
 //
 // A team of 32, 128 or 256 threads holds a row in registers, 8 channels a chunk,
 // so that it is read once; 16 neighbouring lanes hold a block of 128 channels.
+//
+// Both are bound by HBM: 32768 x 7168 with residual and e4m3 rows in 304 us (2.1 GB,
+// 1.03 of the measured copy rate), its gradient in 291 us (1.9 GB, 0.95; with rows
+// through registers alone, two blocks of 128 threads to an SM, 788 us).
 #include <algorithm>
 #include <atomic>
 
@@ -171,7 +175,9 @@ cudaError_t launch_rms_norm(const void *x, const void *residual, const void *wei
 // Rows past 1024 channels are a whole block's.  Their bulk copies go through a ring
 // of stages in shared memory, so that the next rows are on their way while a row
 // waits for its sums; a stage is free again at the sums' barrier, when its values
-// are in registers.  Shorter rows are a warp's, read one row ahead.
+// are in registers.  Shorter rows are a warp's, read one row ahead; up to 512 of them
+// one cluster takes alone, in one launch (259 x 256: 8.1 us a call from Python, with
+// two launches and a workspace 14.7).
 constexpr int kGradTeam = 256;           // threads of a block
 constexpr int kGradStages = 8;           // rows of a ring at most
 constexpr int kNormSms = 152;            // the grids below are sized for

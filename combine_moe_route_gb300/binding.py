@@ -874,13 +874,15 @@ def quantize_mx4(x: torch.Tensor, *, out: torch.Tensor | None = None, out_scale:
     if x.dim() < 1 or x.shape[-1] % 32 or not x.shape[-1]:
         raise ValueError("x must be [..., C] with C a multiple of 32")
     lead, C = tuple(x.shape[:-1]), x.shape[-1]
+    half, blocks = (*lead, C // 2), (*lead, C // 32)
     if out is None:
-        out = torch.empty((*lead, C // 2), dtype=torch.uint8, device=x.device)
+        out = torch.empty(half, dtype=torch.uint8, device=x.device)
     if out_scale is None:
-        out_scale = torch.empty((*lead, C // 32), dtype=torch.uint8, device=x.device)
-    _dev(out, "out", _CODES, (*lead, C // 2))
-    _dev(out_scale, "out_scale", _E8M0, (*lead, C // 32))
-    _on(x, out, out_scale)
+        out_scale = torch.empty(blocks, dtype=torch.uint8, device=x.device)
+    if not _all_fine(x.get_device(), (out, torch.uint8, half), (out_scale, torch.uint8, blocks)):
+        _dev(out, "out", _CODES, half)
+        _dev(out_scale, "out_scale", _E8M0, blocks)
+        _on(x, out, out_scale)
     _enqueue("moe_quantize_mx4", x, stream, x.data_ptr(), _DTYPE_BF16 if x.dtype is torch.bfloat16 else _DTYPE_FP32,
              x.numel() // C, C, out.data_ptr(), out_scale.data_ptr())
     return out, out_scale
@@ -895,12 +897,14 @@ def dequantize_mx4(q: torch.Tensor, scale: torch.Tensor | None, *, out: torch.Te
         raise ValueError("q must be [..., C/2] with C a multiple of 32")
     lead, C = tuple(q.shape[:-1]), 2 * q.shape[-1]
     dtype = torch.float8_e4m3fn if scale is None else torch.bfloat16
-    if scale is not None:
-        _dev(scale, "scale", _E8M0, (*lead, C // 32))
+    full, blocks = (*lead, C), (*lead, C // 32)
     if out is None:
-        out = torch.empty((*lead, C), dtype=dtype, device=q.device)
-    _dev(out, "out", dtype, (*lead, C))
-    _on(q, scale, out)
+        out = torch.empty(full, dtype=dtype, device=q.device)
+    if not _all_fine(q.get_device(), (scale, torch.uint8, blocks), (out, dtype, full)):
+        if scale is not None:
+            _dev(scale, "scale", _E8M0, blocks)
+        _dev(out, "out", dtype, full)
+        _on(q, scale, out)
     _enqueue("moe_dequantize_mx4", q, stream, q.data_ptr(), _ptr(scale), q.numel() // (C // 2), C,
              _DTYPE_FP8 if scale is None else _DTYPE_BF16, out.data_ptr())
     return out
@@ -943,8 +947,9 @@ def expert_gemm_mx4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_s
         raise ValueError("out_dtype must be bfloat16 or float32")
     if out is None:
         out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
-    _dev(out, "out", out_dtype, (rows, N))
-    _on(a, out)
+    if not _all_fine(a.get_device(), (out, out_dtype, (rows, N))):
+        _dev(out, "out", out_dtype, (rows, N))
+        _on(a, out)
     _enqueue("moe_expert_gemm_mx4", a, stream, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
              expert_offsets.data_ptr(), E, N, C, rows, _DTYPE_FP32 if out_dtype is torch.float32 else _DTYPE_BF16,
              out.data_ptr())
@@ -961,13 +966,15 @@ def expert_gated_gemm_mx4(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tenso
     if N % 64:
         raise ValueError("w must be [E, 2*I, C/2] with I a multiple of 32")
     inner, dev = N // 2, a.device
+    half, blocks = (rows, inner // 2), (rows, inner // 32)
     if out is None:
-        out = torch.empty((rows, inner // 2), dtype=torch.uint8, device=dev)
+        out = torch.empty(half, dtype=torch.uint8, device=dev)
     if out_scale is None:
-        out_scale = torch.empty((rows, inner // 32), dtype=torch.uint8, device=dev)
-    _dev(out, "out", _CODES, (rows, inner // 2))
-    _dev(out_scale, "out_scale", _E8M0, (rows, inner // 32))
-    _on(a, out, out_scale)
+        out_scale = torch.empty(blocks, dtype=torch.uint8, device=dev)
+    if not _all_fine(a.get_device(), (out, torch.uint8, half), (out_scale, torch.uint8, blocks)):
+        _dev(out, "out", _CODES, half)
+        _dev(out_scale, "out_scale", _E8M0, blocks)
+        _on(a, out, out_scale)
     _enqueue("moe_expert_gated_gemm_mx4", a, stream, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
              w_scale.data_ptr(), expert_offsets.data_ptr(), E, inner, C, rows, out.data_ptr(), out_scale.data_ptr())
     return GatedResult(out, out_scale, None)

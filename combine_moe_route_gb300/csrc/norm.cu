@@ -449,7 +449,7 @@ static cudaError_t launch_long_rows(NormGradArgs p, int grid, cudaStream_t strea
     if (e != cudaSuccess) return e;
     auto kernel = norm_gradient_kernel<kChunks>;
     const int stage = p.H * (p.dh ? 6 : 4), room = (kChunks <= 4 ? 113 : 226) * 1024 - 512;
-    p.stages = std::min(room / stage, kGradStages);
+    p.stages = std::min((room - 16) / stage, kGradStages);   // 16 bytes to align them
     static std::atomic<uint64_t> ready{0};
     const cudaError_t r = raise_shared_limit(reinterpret_cast<const void *>(kernel), room, ready);
     if (r != cudaSuccess) return r;

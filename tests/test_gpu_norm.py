@@ -117,6 +117,24 @@ def test_gradient(gpu, T, H, residual):
     assert torch.equal(again.dx, got.dx) and torch.equal(again.dweight, got.dweight)
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("H", [1600, 2400, 3600, 4800, 5760, 7200, 9600, 14400])
+def test_gradient_of_rows_that_fill_the_ring(gpu, H, residual):
+    """Rows whose stages take all of the shared memory, or nearly, and more rows than blocks."""
+    from combine_moe_route_gb300 import binding as b
+    gen = torch.Generator(device=gpu).manual_seed(H)
+    T = 700
+    h, dy = _rows(gpu, gen, T, H, 3.0), _rows(gpu, gen, T, H)
+    dh = _rows(gpu, gen, T, H) if residual else None
+    w = _rows(gpu, gen, 1, H)[0]
+    got = b.rms_norm_backward(dy, h, w, dh=dh, eps=EPS)
+    dx, dw, n, g, r = grad64(dy.double(), h.double(), w.double(), dh.double() if residual else None)
+    err = rel_bound(H) * r * (g.abs() + 3 * n.abs() * (g * n).abs().mean(1, keepdim=True))
+    err = err + 2.0 ** -8 * dx.abs() + 2.0 ** -23 * (dx.abs() + (dh.double().abs() if residual else 0))
+    assert ((got.dx.double() - dx).abs() <= err).all()
+    assert ((got.dweight.double() - dw).abs() <= (T * 2.0 ** -24 + rel_bound(H)) * (dy.double() * n).abs().sum(0)).all()
+
+
 def test_gradient_against_differences(gpu):
     """dx and dweight against central differences of the 64-bit norm at the kernel's own bf16 inputs."""
     from combine_moe_route_gb300 import binding as b
